@@ -535,6 +535,187 @@ msa_status msa_rope_cache_build(const msa_dims* dims, int32_t t_loc_max, int32_t
                                 size_t cache_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rotary positions of query and key heads, and their per-head norms.
+ * Pages: IRMaD "M. Materials & Methods", position item (RoPE of the active
+ * context).  msa_rope_rows and msa_sparse_attend rotate whole heads in the half
+ * layout with theta_i = base^(-2i/head_dim); these calls take the position code
+ * of the backbone that the memory serves: its layout, the part of the head it
+ * turns, its frequency scaling for contexts longer than the trained one, and the
+ * RMS norm of every query and key head before the rotation (as the backbone of
+ * the 1M-token workload, with 32 query and 8 key heads of 128, has it).
+ *
+ * msa_rotary, with R = rot_dim and pairs i = 0 .. R/2 - 1:
+ *   layout     MSA_LAYOUT_HALF: pair i is (x_i, x_{i + R/2});
+ *              MSA_LAYOUT_INTERLEAVED: pair i is (x_2i, x_{2i + 1}).
+ *              Elements R .. head_dim - 1 are left alone.
+ *   scaling    the angle of pair i at position p is p theta'_i, theta_i = base^(-2i/R):
+ *     NONE     theta'_i = theta_i
+ *     LINEAR   theta'_i = theta_i / factor (position interpolation)
+ *     NTK      theta_i of the base base * factor^(R/(R-2))
+ *     PARTS    t = orig_len theta_i / 2 pi turns over the trained context,
+ *              g = clamp((t - low) / (high - low), 0, 1):
+ *              theta'_i = (1 - g) theta_i / factor + g theta_i
+ *     YARN     (Peng et al., YaRN) the same mix with a ramp over the pair's index:
+ *              at(t) = R ln(orig_len / (2 pi t)) / (2 ln base),
+ *              first = max(floor(at(high)), 0), last = min(ceil(at(low)), R - 1),
+ *              g = 1 - clamp((i - first) / (last - first), 0, 1) (0.001 for an empty ramp)
+ *   magnitude  multiplies cosine and sine (1 = a plain rotation; YaRN's attention
+ *              temperature is 0.1 ln(factor) + 1).
+ *   Rotation: (a, b) -> m (a cos - b sin, b cos + a sin), m = magnitude.
+ * The frequencies are computed on the host in extended precision; the angle is
+ * reduced exactly (a 64-bit fraction of a turn), whatever the position's size.
+ * Limits: head_dim in [2, 256]; rot_dim even, in [2, head_dim]; base finite > 1;
+ * factor finite >= 1; magnitude finite > 0; for PARTS and YARN orig_len >= 1,
+ * 0 < low < high.
+ *
+ * msa_heads: `heads` heads of each of the call's rows; element (row, head, d) is
+ * at in + row * in_row + head * in_head + d, strides in elements (a slice of a
+ * fused projection works), and likewise out.  out may equal in with the same
+ * strides; otherwise they must not overlap.  Pointers need the alignment of an
+ * element only; the kernels take 16-byte accesses where pointers, strides and
+ * rot_dim allow them.
+ * dtype: type of every head tensor and weight of the call.
+ * ------------------------------------------------------------------------- */
+typedef enum { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype;
+enum { MSA_LAYOUT_HALF = 0, MSA_LAYOUT_INTERLEAVED = 1 };
+enum { MSA_SCALING_NONE = 0, MSA_SCALING_LINEAR = 1, MSA_SCALING_NTK = 2, MSA_SCALING_PARTS = 3, MSA_SCALING_YARN = 4 };
+typedef struct {
+  int32_t head_dim;
+  int32_t rot_dim;
+  int32_t layout;
+  int32_t scaling;
+  int32_t orig_len;
+  int32_t reserved; /* 0 */
+  double base;
+  double factor;
+  double low;
+  double high;
+  double magnitude;
+} msa_rotary;
+typedef struct {
+  const void* in;
+  void* out;
+  int64_t in_row, in_head;
+  int64_t out_row, out_head;
+  int32_t heads;
+  int32_t reserved; /* 0 */
+} msa_heads;
+
+/* turns_out: [rot_dim / 2] host, theta'_i / (2 pi) as 64-bit binary fractions of a turn. */
+msa_status msa_rotary_turns(const msa_rotary* rot, uint64_t* turns_out);
+
+/* Rotate the query heads q and (k != NULL) the key heads k of `rows` rows at
+ * positions [rows] (device int32, any sign).  grad != 0 applies the transposed
+ * rotation m (a cos + b sin, b cos - a sin): the gradient of the call with
+ * respect to its input, given the gradient of its output.  fp32 arithmetic, one
+ * rounding to the output type.  rows >= 0 (0: nothing is launched). */
+msa_status msa_rotate(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k, int64_t rows,
+                      const int32_t* positions, int32_t grad, void* stream);
+
+/* Per-head RMS norm and rotation in one pass:
+ *   n = x / sqrt(mean_d(x_d^2) + eps),  y = Rot(n * (weight_offset + w)),
+ * w = q_weight or k_weight [head_dim] (NULL: the factor is 1; weight_offset is 0, or
+ * 1 for weights stored around 0).  The mean and the rotation in fp32, one rounding.
+ * k may be NULL.  eps >= 0. */
+msa_status msa_head_norm_rotate(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                int64_t rows, const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                const int32_t* positions, void* stream);
+
+/* The decode (or prefill) step's form: the same for q, while each row's key heads,
+ * normalised and rotated, and its value heads v (copied) go to the local cache:
+ * row r belongs to query r / (rows / B) and is written at slot slots[r]:
+ *   K_loc[b, slots[r]] = y_k[r],  V_loc[b, slots[r]] = v[r].
+ * K_loc, V_loc [B, t_loc_max, k->heads, head_dim] of the call's dtype, contiguous;
+ * k->out and v->out are unused.  slots [rows] device int32: -1 leaves the row out
+ * of the cache (a padded row); another slot outside [0, t_loc_max) is left out too
+ * and raises device error bit 1.  Two rows of a query must not share a slot. */
+msa_status msa_head_norm_append(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                const msa_heads* v, int64_t rows, const void* q_weight, const void* k_weight,
+                                float weight_offset, float eps, const int32_t* positions, const int32_t* slots,
+                                void* K_loc, void* V_loc, int32_t B, int32_t t_loc_max, void* stream);
+
+/* Gradients of msa_head_norm_rotate: q->in, k->in are its inputs x, dq and dk the
+ * gradients of its outputs (in) and of its inputs (out):
+ *   z = Rot^T(dy),  u = z (weight_offset + w),  n = x r,  r = 1 / sqrt(mean(x^2) + eps)
+ *   dx = r (u - n mean_d(u n)),  dw_d = sum over rows and heads of z_d n_d.
+ * q->out and k->out are unused; dq->heads == q->heads.  dq_weight, dk_weight: [head_dim] fp32 device out,
+ * each optional (NULL).  k and dk may be NULL together.  The weight sums are taken in a fixed order:
+ * two calls with the same arguments give the same bits on the same GPU.
+ * ws >= msa_head_norm_grad_workspace_size(...) bytes, 256-byte aligned. */
+size_t msa_head_norm_grad_workspace_size(const msa_rotary* rot, int64_t rows, int32_t n_q, int32_t n_k);
+msa_status msa_head_norm_rotate_grad(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                     const msa_heads* dq, const msa_heads* dk, int64_t rows, const void* q_weight,
+                                     const void* k_weight, float weight_offset, float eps, const int32_t* positions,
+                                     float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * A decode step over a tree of drafted tokens.
+ * Pages: IRMaD "M. Materials & Methods", routing item (K_ctx = [selected documents'
+ * K̄; local K]); drafting several continuations and keeping the accepted one
+ * is not on the pages: it lets one pass over the routed memory and the local cache
+ * serve several tokens.  A step: msa_tree_plan (masks and positions),
+ * msa_head_norm_rotate or msa_rotate of the drafts' queries and keys at those
+ * positions, msa_tree_attend, and, once the program has chosen the accepted path,
+ * msa_tree_commit.
+ *
+ * msa_tree_plan
+ *   parents    [B, M] device int32: an earlier draft of the same query, or -1 (the
+ *              draft follows the committed context).  A parent outside [-1, t) raises
+ *              device error bit 1 and counts as -1.
+ *   n_draft    [B] device int32 drafts in use (clamped to [0, M]), or NULL (all M).
+ *   loc_len    [B] device int32 committed local tokens.
+ *   mask       [B, M, ceil(M / 32)] device int32 out: bit j % 32 of word j / 32 of row t
+ *              is set where draft j is t or an ancestor of t; rows t >= n_draft are 0.
+ *   positions  [B, M] device int32 out: pos_offset + loc_len + depth, depth = the number
+ *              of ancestors (0 for rows t >= n_draft).
+ * Limits: 1 <= B <= 65535, 1 <= M <= 256, pos_offset >= 0.
+ * ------------------------------------------------------------------------- */
+msa_status msa_tree_plan(const int32_t* parents, const int32_t* n_draft, const int32_t* loc_len, int32_t B, int32_t M,
+                         int32_t pos_offset, int32_t* mask, int32_t* positions, void* stream);
+
+/* GQA attention of every draft over [selected documents' K̄; local K; the drafts it sees].
+ *   q          [B, M, n_q, head_dim] bf16, ALREADY rotated (nothing is rotated here).
+ *   K_draft, V_draft [B, M, n_kv, head_dim] bf16, keys rotated.
+ *   mask       [B, M, ceil(M / 32)] device int32 as msa_tree_plan writes it (any mask may
+ *              be given: bit j of row t lets draft t see draft j).
+ *   n_draft    [B] device int32 or NULL: drafts t >= n_draft[b] see nothing, are seen by
+ *              nobody, and get a zero row in out.
+ *   K_loc, V_loc [B, t_loc_max, n_kv, head_dim] bf16, keys rotated; loc_len [B] (clamped to
+ *              [0, t_loc_max]); every draft sees the tokens j < loc_len[b].  t_loc_max
+ *              may be 0 (K_loc, V_loc NULL).
+ *   K_bar, V_bar, chunk_off, topk_idx  as msa_sparse_attend; k = 0 leaves the memory out
+ *              (all four NULL).  Every draft sees every pooled row of its query's documents.
+ *   softmax_scale  0 -> 1/sqrt(head_dim).
+ *   out        [B, M, n_q, head_dim] bf16.  A row that sees no key is 0.
+ * Keys and values outside loc_len and n_draft, and of drafts that no row of the query
+ * sees, may hold anything (NaN and infinities included).  A value row that some row of
+ * its query sees must be finite.
+ * Rounding: products of bf16 with fp32 accumulation; softmax statistics fp32; the
+ * weights of the values are rounded to bf16 for the tensor cores.
+ * Limits: head_dim in {64, 128}; n_kv <= 8; n_q / n_kv <= 16; 1 <= M <= 256;
+ * 1 <= B <= 4096; k <= min(n_docs, 256).
+ */
+size_t msa_tree_attend_workspace_size(const msa_dims* dims, int32_t B, int32_t M, int32_t k, int32_t t_loc_max);
+msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_draft, const void* V_draft,
+                           const int32_t* mask, const int32_t* n_draft, int32_t B, int32_t M, const void* K_loc,
+                           const void* V_loc, const int32_t* loc_len, int32_t t_loc_max, const void* K_bar,
+                           const void* V_bar, const int32_t* chunk_off, int32_t n_docs, int32_t n_chunks,
+                           const int32_t* topk_idx, int32_t k, float softmax_scale, void* out, void* ws, size_t ws_bytes,
+                           void* stream);
+
+/* Append the accepted drafts to the local caches: for i < n_path[b] (clamped to [0, A])
+ *   K_loc[b, loc_len[b] + i] = K_draft[b, path[b, i]],  V_loc likewise,
+ *   new_len[b] = loc_len[b] + n_path[b], at most t_loc_max.
+ * A draft at depth i was rotated at the position its row gets here, so no key is
+ * turned again.  path [B, A] device int32, ids in [0, M); an id or a slot outside its
+ * range is left out and raises device error bit 1.  new_len [B] device int32 out must
+ * not be loc_len itself.  Rows behind the last appended one are left as they were.
+ * Limits: 1 <= A <= M <= 256; 1 <= B <= 65535. */
+msa_status msa_tree_commit(const msa_dims* dims, const void* K_draft, const void* V_draft, const int32_t* path,
+                           const int32_t* n_path, int32_t B, int32_t M, int32_t A, void* K_loc, void* V_loc,
+                           const int32_t* loc_len, int32_t t_loc_max, int32_t* new_len, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Tracing: per-kernel device time.
  * While enabled, every kernel launch is bracketed by CUDA events recorded on
  * the stream it is launched on.  msa_trace_read synchronises on those events

@@ -8,7 +8,9 @@ call raises ImportError when the library is missing; there is no CPU fallback.
 
 Entry points (same names as the C ABI, minus the ``msa_`` prefix):
   chunk_offsets, encode_memory, append_memory, route_topk, sparse_attend, kv_append, aux_loss,
-  gather_kv, tiered_decode, *_workspace_size, check_device_errors, trace_*.
+  gather_kv, tiered_decode, rotate, head_norm_rotate, head_norm_append, head_norm_rotate_grad,
+  tree_plan, tree_attend, tree_commit, *_workspace_size, check_device_errors, trace_*.
+``rotary`` builds the description of a position code that the rotation calls take.
 """
 from __future__ import annotations
 
@@ -19,7 +21,9 @@ from typing import Optional
 __all__ = [
     "Dims", "MSAError", "lib", "chunk_offsets", "encode_memory", "append_memory", "route_topk", "sparse_attend",
     "aux_loss", "kv_append", "router_key_norms", "Layer", "tiered_layers", "tiered_workspace_size", "tiered_decode",
-    "sparse_attend_share", "attend_merge",
+    "sparse_attend_share", "attend_merge", "Rotary", "rotary", "rotary_turns", "rotate", "head_norm_rotate",
+    "head_norm_append", "head_norm_rotate_grad", "head_norm_grad_workspace_size", "tree_plan", "tree_attend",
+    "tree_attend_workspace_size", "tree_commit",
     "route_workspace_size", "attend_workspace_size", "rope_cache_build", "topk_merge", "rope_rows", "gather_kv", "encode_workspace_size", "check_device_errors", "selftest_wait_timeout",
     "trace_enable", "trace_reset", "trace_read", "trace_kernel_names", "AGG_MAX", "AGG_MEAN", "ATTEND_EARLY_LOCAL", "ROUTE_EARLY_INPUTS",
 ]
@@ -70,6 +74,21 @@ class Layer(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in _LAYER_FIELDS]
 
 
+class Rotary(ctypes.Structure):
+    """msa_rotary: a position code (see ``rotary``)."""
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("orig_len", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
+
+
+class _Heads(ctypes.Structure):
+    """msa_heads: strided heads of a call's rows, read (inp) and written (out)."""
+    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_row", ctypes.c_int64),
+                ("in_head", ctypes.c_int64), ("out_row", ctypes.c_int64), ("out_head", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -77,7 +96,7 @@ def _load():
             "(nvcc, sm_100a). There is no CPU fallback.")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    DP = ctypes.POINTER(Dims)
+    DP, RP, HP = ctypes.POINTER(Dims), ctypes.POINTER(Rotary), ctypes.POINTER(_Heads)
     sig = {
         "msa_last_error": (ctypes.c_char_p, []),
         "msa_version": (I32, []),
@@ -107,6 +126,16 @@ def _load():
         "msa_rope_cache_size": (SZ, [DP, I32]),
         "msa_rope_cache_build": (I32, [DP, I32, I32, P, SZ, P]),
         "msa_topk_merge": (I32, [P, P, I32, I32, I32, P, P, P]),
+        "msa_rotary_turns": (I32, [RP, P]),
+        "msa_rotate": (I32, [RP, I32, HP, HP, I64, P, I32, P]),
+        "msa_head_norm_rotate": (I32, [RP, I32, HP, HP, I64, P, P, F, F, P, P]),
+        "msa_head_norm_append": (I32, [RP, I32, HP, HP, HP, I64, P, P, F, F, P, P, P, P, I32, I32, P]),
+        "msa_head_norm_grad_workspace_size": (SZ, [RP, I64, I32, I32]),
+        "msa_head_norm_rotate_grad": (I32, [RP, I32, HP, HP, HP, HP, I64, P, P, F, F, P, P, P, P, SZ, P]),
+        "msa_tree_plan": (I32, [P, P, P, I32, I32, I32, P, P, P]),
+        "msa_tree_attend_workspace_size": (SZ, [DP, I32, I32, I32, I32]),
+        "msa_tree_attend": (I32, [DP, P, P, P, P, P, I32, I32, P, P, P, I32, P, P, P, I32, I32, P, I32, F, P, P, SZ, P]),
+        "msa_tree_commit": (I32, [DP, P, P, P, P, I32, I32, I32, P, P, P, I32, P, P]),
         "msa_trace_enable": (I32, [I32]),
         "msa_trace_reset": (I32, []),
         "msa_trace_num_kernels": (I32, []),
@@ -512,6 +541,368 @@ def attend_merge(o_shares, lse2_shares, out=None, stream=None):
         out = torch.empty(tuple(o_shares.shape[1:]), dtype=torch.bfloat16, device=o_shares.device)
     _check(lib.msa_attend_merge(_ptr(o_shares), _ptr(lse2_shares), R, rows, D, _ptr(out), _stream(stream)))
     return out
+
+
+# ----------------------------------------------------------------------------
+# rotary positions and per-head norms
+# ----------------------------------------------------------------------------
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
+_DTYPES: dict = {}  # torch dtype -> msa_dtype (filled on first use: the module imports without torch)
+
+
+def rotary(head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", base: float = 1e6,
+           scaling: str = "none", factor: float = 1.0, orig_len: int = 0, low: float = 1.0, high: float = 32.0,
+           magnitude: float = 1.0) -> Rotary:
+    """A position code for ``rotate`` and the ``head_norm_*`` calls.
+
+    The first ``rot_dim`` (default: all) elements of a head are turned in pairs (i, i + rot_dim/2)
+    (``layout`` "half") or (2i, 2i + 1) ("interleaved") by position * theta_i, theta_i =
+    base^(-2i/rot_dim), ``scaling`` one of "none", "linear", "ntk", "parts" (mixed by turns over
+    ``orig_len`` tokens between ``low`` and ``high``) and "yarn" (the same mix over the pair's
+    index), by ``factor``; cosine and sine are multiplied by ``magnitude`` (see msa.h)."""
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
+    if scaling not in _SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(_SCALINGS)}, got {scaling!r}")
+    return Rotary(head_dim, head_dim if rot_dim is None else rot_dim, _LAYOUTS[layout], _SCALINGS[scaling], orig_len, 0,
+                  base, factor, low, high, magnitude)
+
+
+def rotary_turns(rot: Rotary):
+    """[rot_dim / 2] uint64 (numpy): each pair's turns per position as 64-bit binary fractions."""
+    import numpy as np
+
+    out = np.zeros(max(1, rot.rot_dim // 2), dtype=np.uint64)
+    _check(lib.msa_rotary_turns(ctypes.byref(rot), out.ctypes.data))
+    return out
+
+
+def _dtype_code(dtype, name: str) -> int:
+    if not _DTYPES:
+        import torch
+
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, got {dtype}")
+    return code
+
+
+def _on_device(t, name: str):
+    """The CUDA device of t, which must be the current one (the library launches there)."""
+    import torch
+
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"{name}: expected a CUDA tensor, got {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
+
+
+def _head_shape(t, name: str, rot: Rotary, rows, heads, dtype, device) -> None:
+    """Raise ValueError unless t is [rows, heads, head_dim] with contiguous head elements (rows or
+    heads None: any)."""
+    sh = t.shape
+    if (len(sh) != 3 or sh[2] != rot.head_dim or (rows is not None and sh[0] != rows)
+            or (heads is not None and sh[1] != heads) or sh[1] < 1):
+        raise ValueError(f"{name}: expected [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
+                         f"{rot.head_dim}], got {tuple(sh)}")
+    if t.dtype != dtype or t.device != device or t.stride(2) != 1:
+        raise ValueError(f"{name}: expected {dtype} on {device} with contiguous head elements, got {t.dtype} on "
+                         f"{t.device}, strides {t.stride()}")
+
+
+def _heads(t, out=None) -> _Heads:
+    st = t.stride()
+    if out is None:
+        return _Heads(t.data_ptr(), None, st[0], st[1], 0, 0, t.shape[1], 0)
+    so = out.stride()
+    return _Heads(t.data_ptr(), out.data_ptr(), st[0], st[1], so[0], so[1], t.shape[1], 0)
+
+
+def _used_on(stream, *tensors) -> None:
+    """Tell the allocator that tensors allocated here are used on the caller's ``stream``."""
+    if stream is None:
+        return
+    import torch
+
+    st = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if st != torch.cuda.current_stream():
+        for t in tensors:
+            if t is not None:
+                t.record_stream(st)
+
+
+def _norm_weights(rot, q_weight, k_weight, dtype, device) -> None:
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _expect(w, name, (rot.head_dim,), dtype, device)
+
+
+def _rot_args(rot, q, k, positions, out, k_out):
+    """Checks shared by the rotation and norm calls; allocates missing outputs."""
+    import torch
+
+    dev = _on_device(q, "q")
+    code = _dtype_code(q.dtype, "q")
+    _head_shape(q, "q", rot, None, None, q.dtype, dev)
+    rows = q.shape[0]
+    _expect(positions, "positions", (rows,), torch.int32, dev)
+    new = []
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=q.dtype, device=dev)
+        new.append(out)
+    else:
+        _head_shape(out, "out", rot, rows, q.shape[1], q.dtype, dev)
+    if k is not None:
+        _head_shape(k, "k", rot, rows, None, q.dtype, dev)
+        if k_out is None:
+            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=dev)
+            new.append(k_out)
+        else:
+            _head_shape(k_out, "k_out", rot, rows, k.shape[1], q.dtype, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    return code, rows, out, k_out, new
+
+
+def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_out=None, stream=None):
+    """Rotate query heads q (and key heads k) [rows, heads, head_dim] at ``positions`` [rows] int32.
+
+    bf16, fp16 or fp32; rows and heads may be strided (slices of a fused projection).  ``out`` /
+    ``k_out`` may be q / k themselves (in place).  ``grad`` applies the transposed rotation: the
+    gradient of the call, given the gradient of its output.  Returns out, or (out, k_out) with k."""
+    code, rows, out, k_out, new = _rot_args(rot, q, k, positions, out, k_out)
+    _check(lib.msa_rotate(ctypes.byref(rot), code, _heads(q, out), None if k is None else _heads(k, k_out), rows,
+                          positions.data_ptr(), 1 if grad else 0, _stream(stream)))
+    _used_on(stream, *new)
+    return out if k is None else (out, k_out)
+
+
+def head_norm_rotate(rot: Rotary, q, k, q_weight, k_weight, positions, eps: float = 1e-6, weight_offset: float = 0.0,
+                     out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head, times (weight_offset + weight), then the rotation, in
+    one pass.  q, k [rows, heads, head_dim] as for ``rotate`` (k may be None); weights [head_dim] of
+    the same dtype, or None.  Returns (out, k_out), or out without k."""
+    code, rows, out, k_out, new = _rot_args(rot, q, k, positions, out, k_out)
+    _norm_weights(rot, q_weight, k_weight, q.dtype, q.device)
+    _check(lib.msa_head_norm_rotate(ctypes.byref(rot), code, _heads(q, out), None if k is None else _heads(k, k_out),
+                                    rows, _ptr(q_weight), _ptr(k_weight), weight_offset, eps, positions.data_ptr(),
+                                    _stream(stream)))
+    _used_on(stream, *new)
+    return out if k is None else (out, k_out)
+
+
+def head_norm_append(rot: Rotary, q, k, v, q_weight, k_weight, positions, slots, K_loc, V_loc, eps: float = 1e-6,
+                     weight_offset: float = 0.0, out=None, stream=None):
+    """``head_norm_rotate`` of a decode or prefill step: the queries go to ``out``, the keys
+    (normalised, rotated) and the values to row ``slots[r]`` of their query's local cache
+    K_loc, V_loc [B, t_loc_max, n_kv, head_dim] (rows / B rows per query, in order).  A slot of -1
+    leaves the row out of the cache.  Returns out."""
+    import torch
+
+    code, rows, out, _, new = _rot_args(rot, q, None, positions, out, None)
+    dt, dev = q.dtype, q.device
+    _head_shape(k, "k", rot, rows, None, dt, dev)
+    _head_shape(v, "v", rot, rows, k.shape[1], dt, dev)
+    _norm_weights(rot, q_weight, k_weight, dt, dev)
+    _expect(slots, "slots", (rows,), torch.int32, dev)
+    if K_loc.dim() != 4:
+        raise ValueError(f"K_loc: expected [B, t_loc_max, n_kv, head_dim], got {tuple(K_loc.shape)}")
+    B, t_loc_max = K_loc.shape[0], K_loc.shape[1]
+    for name, t in (("K_loc", K_loc), ("V_loc", V_loc)):
+        _expect(t, name, (B, t_loc_max, k.shape[1], rot.head_dim), dt, dev)
+    _check(lib.msa_head_norm_append(ctypes.byref(rot), code, _heads(q, out), _heads(k), _heads(v), rows, _ptr(q_weight),
+                                    _ptr(k_weight), weight_offset, eps, positions.data_ptr(), slots.data_ptr(),
+                                    K_loc.data_ptr(), V_loc.data_ptr(), B, t_loc_max, _stream(stream)))
+    _used_on(stream, *new)
+    return out
+
+
+def head_norm_grad_workspace_size(rot: Rotary, rows: int, n_q: int, n_k: int) -> int:
+    return int(lib.msa_head_norm_grad_workspace_size(ctypes.byref(rot), rows, n_q, n_k))
+
+
+def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, dk, eps: float = 1e-6,
+                          weight_offset: float = 0.0, out=None, ws=None, stream=None):
+    """Gradients of ``head_norm_rotate`` at its inputs q, k given those of its outputs, dq, dk.
+
+    Returns (gradient of q, of k, of q_weight [head_dim] fp32, of k_weight fp32); ``out`` takes the
+    four tensors.  k and dk may be None together (the second and fourth are then None)."""
+    import torch
+
+    if (k is None) != (dk is None):
+        raise ValueError("k and dk go together")
+    o = (None,) * 4 if out is None else out
+    code, rows, gq, gk, new = _rot_args(rot, q, k, positions, o[0], o[1])
+    dt, dev = q.dtype, q.device
+    _head_shape(dq, "dq", rot, rows, q.shape[1], dt, dev)
+    if dk is not None:
+        _head_shape(dk, "dk", rot, rows, k.shape[1], dt, dev)
+    _norm_weights(rot, q_weight, k_weight, dt, dev)
+    dw = []
+    for name, t, used in (("out[2]", o[2], True), ("out[3]", o[3], k is not None)):
+        if t is None and used:
+            t = torch.empty(rot.head_dim, dtype=torch.float32, device=dev)
+            new.append(t)
+        elif t is not None:
+            _expect(t, name, (rot.head_dim,), torch.float32, dev)
+        dw.append(t)
+    nbytes = head_norm_grad_workspace_size(rot, rows, q.shape[1], 0 if k is None else k.shape[1])
+    if ws is None:
+        ws = _workspace(nbytes, dev)
+        new.append(ws)
+    else:  # the library checks the caller's buffer against what it needs
+        nbytes = max(0, ws.numel() * ws.element_size() - 256)
+    _check(lib.msa_head_norm_rotate_grad(
+        ctypes.byref(rot), code, _heads(q), None if k is None else _heads(k), _heads(dq, gq),
+        None if k is None else _heads(dk, gk), rows, _ptr(q_weight), _ptr(k_weight), weight_offset, eps,
+        positions.data_ptr(), _ptr(dw[0]), _ptr(dw[1]), _aligned_ptr(ws), nbytes, _stream(stream)))
+    _used_on(stream, *new)
+    return gq, gk, dw[0], dw[1]
+
+
+# ----------------------------------------------------------------------------
+# a decode step over a tree of drafted tokens
+# ----------------------------------------------------------------------------
+def tree_plan(parents, loc_len, pos_offset: int, n_draft=None, out=None, stream=None):
+    """(mask [B, M, ceil(M/32)] int32, positions [B, M] int32) of trees of drafts.
+
+    ``parents`` [B, M] int32: an earlier draft, or -1 for one that follows the committed context of
+    ``loc_len`` [B] tokens; ``n_draft`` [B] int32: drafts in use (None: all)."""
+    import torch
+
+    dev = _on_device(parents, "parents")
+    if parents.dim() != 2:
+        raise ValueError(f"parents: expected [B, M], got {tuple(parents.shape)}")
+    B, M = parents.shape
+    _expect(parents, "parents", (B, M), torch.int32, dev)
+    _expect(loc_len, "loc_len", (B,), torch.int32, dev)
+    if n_draft is not None:
+        _expect(n_draft, "n_draft", (B,), torch.int32, dev)
+    new = ()
+    if out is None:
+        out = new = (torch.empty((B, M, (M + 31) // 32), dtype=torch.int32, device=dev),
+                     torch.empty((B, M), dtype=torch.int32, device=dev))
+    else:
+        _expect(out[0], "out[0]", (B, M, (M + 31) // 32), torch.int32, dev)
+        _expect(out[1], "out[1]", (B, M), torch.int32, dev)
+    _check(lib.msa_tree_plan(parents.data_ptr(), _ptr(n_draft), loc_len.data_ptr(), B, M, pos_offset, out[0].data_ptr(),
+                             out[1].data_ptr(), _stream(stream)))
+    _used_on(stream, *new)
+    return out
+
+
+def tree_attend_workspace_size(dims, B: int, M: int, k: int, t_loc_max: int) -> int:
+    return int(lib.msa_tree_attend_workspace_size(ctypes.byref(Dims.of(dims)), B, M, k, t_loc_max))
+
+
+def tree_attend(dims, q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft=None, K_bar=None, V_bar=None,
+                chunk_off=None, topk_idx=None, softmax_scale: float = 0.0, out=None, ws=None, stream=None):
+    """GQA attention of drafted tokens over [routed documents' pooled rows; local cache; the drafts
+    that each sees].
+
+    q [B, M, n_q, head_dim], K_draft, V_draft [B, M, n_kv, head_dim], K_loc, V_loc [B, t_loc_max,
+    n_kv, head_dim] bf16; queries and keys ALREADY rotated (``head_norm_rotate`` or ``rotate`` at
+    ``tree_plan``'s positions).  ``mask`` [B, M, ceil(M/32)] int32 from ``tree_plan``.  The memory
+    arguments (as for ``sparse_attend``) go together; without them the drafts attend over cache and
+    drafts alone.  A draft t >= n_draft[b] and a row that sees no key give zeros."""
+    import torch
+
+    dd = Dims.of(dims)
+    dev = _on_device(q, "q")
+    if q.dim() != 4:
+        raise ValueError(f"q: expected [B, M, n_q, head_dim], got {tuple(q.shape)}")
+    B, M = q.shape[0], q.shape[1]
+    bf, i32 = torch.bfloat16, torch.int32
+    kv = (dd.n_kv, dd.head_dim)
+    _expect(q, "q", (B, M, dd.n_q, dd.head_dim), bf, dev)
+    _expect(K_draft, "K_draft", (B, M) + kv, bf, dev)
+    _expect(V_draft, "V_draft", (B, M) + kv, bf, dev)
+    _expect(mask, "mask", (B, M, (M + 31) // 32), i32, dev)
+    _expect(loc_len, "loc_len", (B,), i32, dev)
+    if n_draft is not None:
+        _expect(n_draft, "n_draft", (B,), i32, dev)
+    t_loc_max = 0
+    if (K_loc is None) != (V_loc is None):
+        raise ValueError("K_loc and V_loc go together")
+    if K_loc is not None:
+        t_loc_max = K_loc.shape[1] if K_loc.dim() == 4 else -1
+        _expect(K_loc, "K_loc", (B, t_loc_max) + kv, bf, dev)
+        _expect(V_loc, "V_loc", (B, t_loc_max) + kv, bf, dev)
+    memory = (K_bar, V_bar, chunk_off, topk_idx)
+    k = n_docs = n_chunks = 0
+    if any(x is not None for x in memory):
+        if any(x is None for x in memory):
+            raise ValueError("K_bar, V_bar, chunk_off and topk_idx go together")
+        k, n_docs, n_chunks = topk_idx.shape[-1], chunk_off.numel() - 1, K_bar.shape[0]
+        _expect(K_bar, "K_bar", (n_chunks,) + kv, bf, dev)
+        _expect(V_bar, "V_bar", (n_chunks,) + kv, bf, dev)
+        _expect(chunk_off, "chunk_off", (n_docs + 1,), i32, dev)
+        _expect(topk_idx, "topk_idx", (B, k), i32, dev)
+        if k == 0:
+            K_bar = V_bar = chunk_off = topk_idx = None
+    new = []
+    if out is None:
+        out = torch.empty(tuple(q.shape), dtype=bf, device=dev)
+        new.append(out)
+    else:
+        _expect(out, "out", tuple(q.shape), bf, dev)
+    if ws is not None:  # the library checks the caller's buffer against what it needs
+        nbytes = max(0, ws.numel() * ws.element_size() - 256)
+    else:
+        nbytes = tree_attend_workspace_size(dims, B, M, k, t_loc_max)
+        ws = _workspace(nbytes, dev)
+        new.append(ws)
+    _check(lib.msa_tree_attend(ctypes.byref(dd), q.data_ptr(), K_draft.data_ptr(), V_draft.data_ptr(), mask.data_ptr(),
+                               _ptr(n_draft), B, M, _ptr(K_loc) if t_loc_max else None,
+                               _ptr(V_loc) if t_loc_max else None, loc_len.data_ptr(), t_loc_max, _ptr(K_bar),
+                               _ptr(V_bar), _ptr(chunk_off), n_docs, n_chunks, _ptr(topk_idx), k, float(softmax_scale),
+                               out.data_ptr(), _aligned_ptr(ws), nbytes, _stream(stream)))
+    _used_on(stream, *new)
+    return out
+
+
+def tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out=None, stream=None):
+    """Append the accepted drafts to the local caches: row path[b, i] of K_draft / V_draft
+    [B, M, n_kv, head_dim] to slot loc_len[b] + i of K_loc / V_loc, for i < n_path[b].  Returns the
+    new lengths [B] int32 (``out``, which must not be ``loc_len``)."""
+    import torch
+
+    dev = _on_device(K_draft, "K_draft")
+    if K_draft.dim() != 4 or K_loc.dim() != 4 or path.dim() != 2:
+        raise ValueError("expected K_draft [B, M, n_kv, head_dim], K_loc [B, t_loc_max, n_kv, head_dim], path [B, A]")
+    B, M, n_kv, D = K_draft.shape
+    t_loc_max, A = K_loc.shape[1], path.shape[1]
+    bf, i32 = torch.bfloat16, torch.int32
+    for name, t, n in (("K_draft", K_draft, M), ("V_draft", V_draft, M), ("K_loc", K_loc, t_loc_max),
+                       ("V_loc", V_loc, t_loc_max)):
+        _expect(t, name, (B, n, n_kv, D), bf, dev)
+    _expect(path, "path", (B, A), i32, dev)
+    _expect(n_path, "n_path", (B,), i32, dev)
+    _expect(loc_len, "loc_len", (B,), i32, dev)
+    new = ()
+    if out is None:
+        out = torch.empty(B, dtype=i32, device=dev)
+        new = (out,)
+    else:
+        _expect(out, "out", (B,), i32, dev)
+    _check(lib.msa_tree_commit(ctypes.byref(_kv_dims(n_kv, D)), K_draft.data_ptr(), V_draft.data_ptr(), path.data_ptr(),
+                               n_path.data_ptr(), B, M, A, K_loc.data_ptr(), V_loc.data_ptr(), loc_len.data_ptr(),
+                               t_loc_max, out.data_ptr(), _stream(stream)))
+    _used_on(stream, *new)
+    return out
+
+
+def _kv_dims(n_kv: int, head_dim: int) -> Dims:
+    """A dims struct of which only the KV heads matter."""
+    key = ("kv", n_kv, head_dim)
+    hit = _DIMS_CACHE.get(key)
+    if hit is None:
+        hit = _DIMS_CACHE[key] = Dims(64, n_kv, n_kv, head_dim, 1, 64, 64, 1e6)
+    return hit
 
 
 # ----------------------------------------------------------------------------

@@ -55,6 +55,14 @@ enum KernelId : int {
   kKKrNorms,
   kKAttnMerge,
   kKChunkDoc,
+  kKRotate,
+  kKHeadNorm,
+  kKHeadNormGrad,
+  kKHeadNormSum,
+  kKTreePlan,
+  kKTreeAttend,
+  kKTreeCombine,
+  kKTreeCommit,
   kKernelCount
 };
 
@@ -247,6 +255,49 @@ msa_status rope_cache_build(const msa_dims& d, int t_loc_max, int pos_offset, fl
 
 msa_status kv_append_launch(const msa_dims& d, const void* k_new, const void* v_new, void* K_loc, void* V_loc, int B,
                             int t_loc_max, const int32_t* slots, int pos_offset, cudaStream_t s);
+// rotary.cu: one call of the rotation and norm kernels.  mode 0: rotation, 1: norm and rotation
+// (slots != null: keys and values into the cache), 2: the norms' gradients
+struct RotaryCall {
+  int mode;
+  bool grad;  // mode 0: the transposed rotation
+  const msa_heads *q, *k, *v, *dq, *dk;
+  int64_t rows, rows_per_query;
+  const void *q_weight, *k_weight;
+  float weight_offset, eps;
+  const int32_t *positions, *slots;
+  void *K_loc, *V_loc;
+  int t_loc_max;
+  float *dq_weight, *dk_weight;
+  void* ws;
+};
+void rotary_turns(const msa_rotary& r, uint64_t* f /* [rot_dim / 2] */);
+size_t norm_grad_workspace(const msa_rotary& r, int64_t rows, int n_heads);
+msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall& c, cudaStream_t s);
+
+// tree.cu: a decode step over a tree of drafted tokens
+msa_status tree_plan_launch(const int32_t* parents, const int32_t* n_draft, const int32_t* loc_len, int B, int M,
+                            int pos_offset, int32_t* mask, int32_t* positions, cudaStream_t s);
+size_t tree_attend_workspace(const msa_dims& d, int B, int M, int k, int t_loc_max);
+struct TreeAttendCall {
+  const void *q, *K_draft, *V_draft;
+  const int32_t *mask, *n_draft;
+  int B, M;
+  const void *K_loc, *V_loc;
+  const int32_t* loc_len;
+  int t_loc_max;
+  const void *K_bar, *V_bar;
+  const int32_t* chunk_off;
+  int n_docs, n_chunks;
+  const int32_t* topk_idx;
+  int k;
+  float scale;
+  void *out, *ws;
+};
+msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaStream_t s);
+msa_status tree_commit_launch(const msa_dims& d, const void* K_draft, const void* V_draft, const int32_t* path,
+                              const int32_t* n_path, int B, int M, int A, void* K_loc, void* V_loc,
+                              const int32_t* loc_len, int t_loc_max, int32_t* new_len, cudaStream_t s);
+
 struct AuxWs {
   float* term;        // [P] per-positive loss terms
   uint32_t* ticket;   // CTAs finished

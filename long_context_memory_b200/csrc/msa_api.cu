@@ -219,7 +219,8 @@ namespace {
 const char* kKernelNames[kKernelCount] = {
     "router_query", "scan", "topk_slice", "topk_merge", "rope_table", "attn_split", "attn_combine",
     "enc_chunk_map", "enc_transpose_w", "enc_gemm_k", "enc_pool_h", "enc_gemm_pooled", "rope_rows", "gather_plan", "gather_copy",
-    "chunk_off_extend", "aux_loss", "kv_append", "kr_norms", "attn_merge", "chunk_doc"};
+    "chunk_off_extend", "aux_loss", "kv_append", "kr_norms", "attn_merge", "chunk_doc",
+    "rotate", "head_norm", "head_norm_grad", "head_norm_sum", "tree_plan", "tree_attend", "tree_combine", "tree_commit"};
 
 struct TraceState {
   std::mutex mu;
@@ -870,6 +871,313 @@ msa_status msa_append_memory(const msa_dims* dims, const void* H_new, int64_t T_
   if (st != MSA_OK) return st;
   return chunk_off_extend_launch(chunk_off, n_docs_old, n_chunks_old, chunk_off_new, n_docs_new,
                                  static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------ rotary positions, per-head norms ------------------------------
+static msa_status check_rotary(const msa_rotary* r, msa_dtype dtype) {
+  if (!r) return fail(MSA_ERR_INVALID_ARG, "rot is NULL");
+  if (dtype != MSA_BF16 && dtype != MSA_FP16 && dtype != MSA_FP32)
+    return fail(MSA_ERR_INVALID_ARG, "unknown dtype %d", (int)dtype);
+  if (r->head_dim < 2 || r->head_dim > 256)
+    return fail(MSA_ERR_UNSUPPORTED, "head_dim must be in [2, 256] (got %d)", r->head_dim);
+  if (r->rot_dim < 2 || r->rot_dim > r->head_dim || r->rot_dim % 2 != 0)
+    return fail(MSA_ERR_INVALID_ARG, "rot_dim must be even, in [2, head_dim] (got %d)", r->rot_dim);
+  if (r->layout != MSA_LAYOUT_HALF && r->layout != MSA_LAYOUT_INTERLEAVED)
+    return fail(MSA_ERR_INVALID_ARG, "unknown layout %d", r->layout);
+  if (r->scaling < MSA_SCALING_NONE || r->scaling > MSA_SCALING_YARN)
+    return fail(MSA_ERR_INVALID_ARG, "unknown scaling %d", r->scaling);
+  if (!(r->base > 1.0) || !std::isfinite(r->base)) return fail(MSA_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (!(r->factor >= 1.0) || !std::isfinite(r->factor))
+    return fail(MSA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (!(r->magnitude > 0.0) || !std::isfinite(r->magnitude))
+    return fail(MSA_ERR_INVALID_ARG, "magnitude must be finite and > 0");
+  if (r->scaling >= MSA_SCALING_PARTS &&
+      (r->orig_len < 1 || !(r->low > 0.0) || !(r->high > r->low) || !std::isfinite(r->high)))
+    return fail(MSA_ERR_INVALID_ARG, "this scaling needs orig_len >= 1 and 0 < low < high");
+  return MSA_OK;
+}
+
+static bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
+
+// one msa_heads argument: its input, and its output where the call writes one
+static msa_status check_heads(const msa_heads* h, const char* name, const msa_rotary* r, msa_dtype dtype, int64_t rows,
+                              bool needs_in, bool needs_out) {
+  if (!h) return fail(MSA_ERR_INVALID_ARG, "%s is NULL", name);
+  const size_t size = dtype == MSA_FP32 ? 4 : 2;
+  if (h->heads < 1 || h->heads > 65535) return fail(MSA_ERR_INVALID_ARG, "%s: heads must be in [1, 65535] (got %d)", name, h->heads);
+  if (rows == 0) return MSA_OK;
+  if (needs_in) {
+    if (!h->in || misaligned(h->in, size)) return fail(MSA_ERR_INVALID_ARG, "%s: in is NULL or not aligned to its type", name);
+    if (h->in_row < 0 || h->in_head < 0) return fail(MSA_ERR_INVALID_ARG, "%s: strides must be >= 0", name);
+  }
+  if (needs_out) {
+    if (!h->out || misaligned(h->out, size))
+      return fail(MSA_ERR_INVALID_ARG, "%s: out is NULL or not aligned to its type", name);
+    // no two elements of the output may share a place
+    const int64_t D = r->head_dim;
+    const bool many_r = rows > 1, many_h = h->heads > 1;
+    bool ok = (!many_r || h->out_row >= D) && (!many_h || h->out_head >= D);
+    if (ok && many_r && many_h)
+      ok = h->out_row >= h->out_head ? h->out_row >= h->out_head * (h->heads - 1) + D
+                                     : h->out_head >= h->out_row * (rows - 1) + D;
+    if (!ok) return fail(MSA_ERR_INVALID_ARG, "%s: output heads overlap (strides %lld, %lld)", name,
+                         (long long)h->out_row, (long long)h->out_head);
+    if (needs_in && h->in == h->out && ((many_r && h->in_row != h->out_row) || (many_h && h->in_head != h->out_head)))
+      return fail(MSA_ERR_INVALID_ARG, "%s: an in-place call needs equal strides", name);
+  }
+  return MSA_OK;
+}
+
+static msa_status check_norm(const void* qw, const void* kw, float off, float eps, msa_dtype dtype) {
+  const size_t size = dtype == MSA_FP32 ? 4 : 2;
+  if ((qw && misaligned(qw, size)) || (kw && misaligned(kw, size)))
+    return fail(MSA_ERR_INVALID_ARG, "a norm weight is not aligned to its type");
+  if (!std::isfinite(off)) return fail(MSA_ERR_INVALID_ARG, "weight_offset must be finite");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MSA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  return MSA_OK;
+}
+
+static msa_status check_rows(int64_t rows, const int32_t* positions) {
+  if (rows < 0 || rows > (int64_t)INT32_MAX) return fail(MSA_ERR_INVALID_ARG, "rows must be in [0, 2^31) (got %lld)", (long long)rows);
+  if (rows > 0 && (!positions || misaligned(positions, 4)))
+    return fail(MSA_ERR_INVALID_ARG, "positions is NULL or not 4-byte aligned");
+  return MSA_OK;
+}
+
+#define CHECK_STATUS(expr)             \
+  do {                                 \
+    msa_status st_ = (expr);           \
+    if (st_ != MSA_OK) return st_;     \
+  } while (0)
+
+msa_status msa_rotary_turns(const msa_rotary* rot, uint64_t* turns_out) {
+  CHECK_STATUS(check_rotary(rot, MSA_BF16));
+  if (!turns_out) return fail(MSA_ERR_INVALID_ARG, "turns_out is NULL");
+  rotary_turns(*rot, turns_out);
+  return MSA_OK;
+}
+
+msa_status msa_rotate(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k, int64_t rows,
+                      const int32_t* positions, int32_t grad, void* stream) {
+  CHECK_STATUS(check_rotary(rot, dtype));
+  CHECK_STATUS(check_rows(rows, positions));
+  CHECK_STATUS(check_heads(q, "q", rot, dtype, rows, true, true));
+  if (k) CHECK_STATUS(check_heads(k, "k", rot, dtype, rows, true, true));
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  if (rows == 0) return MSA_OK;
+  RotaryCall c{};
+  c.grad = grad != 0;
+  c.q = q;
+  c.k = k;
+  c.rows = rows;
+  c.positions = positions;
+  return rotary_launch(*rot, dtype, c, static_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_head_norm_rotate(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                int64_t rows, const void* q_weight, const void* k_weight, float weight_offset, float eps,
+                                const int32_t* positions, void* stream) {
+  CHECK_STATUS(check_rotary(rot, dtype));
+  CHECK_STATUS(check_rows(rows, positions));
+  CHECK_STATUS(check_heads(q, "q", rot, dtype, rows, true, true));
+  if (k) CHECK_STATUS(check_heads(k, "k", rot, dtype, rows, true, true));
+  CHECK_STATUS(check_norm(q_weight, k_weight, weight_offset, eps, dtype));
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  if (rows == 0) return MSA_OK;
+  RotaryCall c{};
+  c.mode = 1;
+  c.q = q;
+  c.k = k;
+  c.rows = rows;
+  c.q_weight = q_weight;
+  c.k_weight = k_weight;
+  c.weight_offset = weight_offset;
+  c.eps = eps;
+  c.positions = positions;
+  return rotary_launch(*rot, dtype, c, static_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_head_norm_append(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                const msa_heads* v, int64_t rows, const void* q_weight, const void* k_weight,
+                                float weight_offset, float eps, const int32_t* positions, const int32_t* slots,
+                                void* K_loc, void* V_loc, int32_t B, int32_t t_loc_max, void* stream) {
+  CHECK_STATUS(check_rotary(rot, dtype));
+  CHECK_STATUS(check_rows(rows, positions));
+  CHECK_STATUS(check_heads(q, "q", rot, dtype, rows, true, true));
+  CHECK_STATUS(check_heads(k, "k", rot, dtype, rows, true, false));
+  CHECK_STATUS(check_heads(v, "v", rot, dtype, rows, true, false));
+  if (v->heads != k->heads) return fail(MSA_ERR_INVALID_ARG, "k and v have %d and %d heads", k->heads, v->heads);
+  CHECK_STATUS(check_norm(q_weight, k_weight, weight_offset, eps, dtype));
+  if (B < 1 || t_loc_max < 1) return fail(MSA_ERR_INVALID_ARG, "B and t_loc_max must be >= 1 (got %d, %d)", B, t_loc_max);
+  if (rows % B != 0) return fail(MSA_ERR_INVALID_ARG, "rows (%lld) must be a multiple of B (%d)", (long long)rows, B);
+  const size_t size = dtype == MSA_FP32 ? 4 : 2;
+  if (rows > 0) {
+    if (!slots || misaligned(slots, 4)) return fail(MSA_ERR_INVALID_ARG, "slots is NULL or not 4-byte aligned");
+    if (!K_loc || !V_loc || misaligned(K_loc, size) || misaligned(V_loc, size))
+      return fail(MSA_ERR_INVALID_ARG, "K_loc or V_loc is NULL or not aligned to its type");
+  }
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  if (rows == 0) return MSA_OK;
+  RotaryCall c{};
+  c.mode = 1;
+  c.q = q;
+  c.k = k;
+  c.v = v;
+  c.rows = rows;
+  c.rows_per_query = rows / B;
+  c.q_weight = q_weight;
+  c.k_weight = k_weight;
+  c.weight_offset = weight_offset;
+  c.eps = eps;
+  c.positions = positions;
+  c.slots = slots;
+  c.K_loc = K_loc;
+  c.V_loc = V_loc;
+  c.t_loc_max = t_loc_max;
+  return rotary_launch(*rot, dtype, c, static_cast<cudaStream_t>(stream));
+}
+
+size_t msa_head_norm_grad_workspace_size(const msa_rotary* rot, int64_t rows, int32_t n_q, int32_t n_k) {
+  if (!rot || rot->head_dim < 2 || rot->head_dim > 256 || rows < 0 || n_q < 1 || n_q > 65535 || n_k < 0 || n_k > 65535)
+    return 0;
+  return norm_grad_workspace(*rot, rows, n_q + n_k);
+}
+
+msa_status msa_head_norm_rotate_grad(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
+                                     const msa_heads* dq, const msa_heads* dk, int64_t rows, const void* q_weight,
+                                     const void* k_weight, float weight_offset, float eps, const int32_t* positions,
+                                     float* dq_weight, float* dk_weight, void* ws, size_t ws_bytes, void* stream) {
+  CHECK_STATUS(check_rotary(rot, dtype));
+  CHECK_STATUS(check_rows(rows, positions));
+  CHECK_STATUS(check_heads(q, "q", rot, dtype, rows, true, false));
+  CHECK_STATUS(check_heads(dq, "dq", rot, dtype, rows, true, true));
+  if ((k == nullptr) != (dk == nullptr)) return fail(MSA_ERR_INVALID_ARG, "k and dk go together");
+  if (dq->heads != q->heads) return fail(MSA_ERR_INVALID_ARG, "q and dq have %d and %d heads", q->heads, dq->heads);
+  if (k) {
+    CHECK_STATUS(check_heads(k, "k", rot, dtype, rows, true, false));
+    CHECK_STATUS(check_heads(dk, "dk", rot, dtype, rows, true, true));
+    if (dk->heads != k->heads) return fail(MSA_ERR_INVALID_ARG, "k and dk have %d and %d heads", k->heads, dk->heads);
+  }
+  CHECK_STATUS(check_norm(q_weight, k_weight, weight_offset, eps, dtype));
+  CHECK_OPT_PTR(dq_weight);
+  CHECK_OPT_PTR(dk_weight);
+  if (dk_weight && !k) return fail(MSA_ERR_INVALID_ARG, "dk_weight without k");
+  const size_t need = norm_grad_workspace(*rot, rows, q->heads + (k ? k->heads : 0));
+  if (ws_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  if (!ws || misaligned(ws, 256)) return fail(MSA_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dq_weight) MSA_CUDA_CHECK(cudaMemsetAsync(dq_weight, 0, sizeof(float) * rot->head_dim, s));
+    if (dk_weight) MSA_CUDA_CHECK(cudaMemsetAsync(dk_weight, 0, sizeof(float) * rot->head_dim, s));
+    return MSA_OK;
+  }
+  RotaryCall c{};
+  c.mode = 2;
+  c.q = q;
+  c.k = k;
+  c.dq = dq;
+  c.dk = dk;
+  c.rows = rows;
+  c.q_weight = q_weight;
+  c.k_weight = k_weight;
+  c.weight_offset = weight_offset;
+  c.eps = eps;
+  c.positions = positions;
+  c.dq_weight = dq_weight;
+  c.dk_weight = dk_weight;
+  c.ws = ws;
+  return rotary_launch(*rot, dtype, c, s);
+}
+
+// ------------------------------ trees of drafted tokens ------------------------------
+constexpr int kTreeMaxDrafts = 256;
+
+msa_status msa_tree_plan(const int32_t* parents, const int32_t* n_draft, const int32_t* loc_len, int32_t B, int32_t M,
+                         int32_t pos_offset, int32_t* mask, int32_t* positions, void* stream) {
+  if (B < 1 || B > 65535) return fail(MSA_ERR_INVALID_ARG, "B must be in [1, 65535] (got %d)", B);
+  if (M < 1 || M > kTreeMaxDrafts) return fail(MSA_ERR_INVALID_ARG, "M must be in [1, %d] (got %d)", kTreeMaxDrafts, M);
+  if (pos_offset < 0) return fail(MSA_ERR_INVALID_ARG, "pos_offset must be >= 0 (got %d)", pos_offset);
+  CHECK_PTR(parents);
+  CHECK_OPT_PTR(n_draft);
+  CHECK_PTR(loc_len);
+  CHECK_PTR(mask);
+  CHECK_PTR(positions);
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  return tree_plan_launch(parents, n_draft, loc_len, B, M, pos_offset, mask, positions, static_cast<cudaStream_t>(stream));
+}
+
+size_t msa_tree_attend_workspace_size(const msa_dims* dims, int32_t B, int32_t M, int32_t k, int32_t t_loc_max) {
+  if (!dims || dims->n_kv < 1 || dims->n_kv > 8 || dims->n_q < dims->n_kv || dims->n_q % dims->n_kv != 0 ||
+      dims->n_q / dims->n_kv > 16 || (dims->head_dim != 64 && dims->head_dim != 128) || B < 1 || B > 4096 || M < 1 ||
+      M > kTreeMaxDrafts || k < 0 || k > 256 || t_loc_max < 0)
+    return 0;
+  return tree_attend_workspace(*dims, B, M, k, t_loc_max);
+}
+
+msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_draft, const void* V_draft,
+                           const int32_t* mask, const int32_t* n_draft, int32_t B, int32_t M, const void* K_loc,
+                           const void* V_loc, const int32_t* loc_len, int32_t t_loc_max, const void* K_bar,
+                           const void* V_bar, const int32_t* chunk_off, int32_t n_docs, int32_t n_chunks,
+                           const int32_t* topk_idx, int32_t k, float softmax_scale, void* out, void* ws, size_t ws_bytes,
+                           void* stream) {
+  CHECK_STATUS(check_dims(dims, true, false));
+  if (B < 1 || B > 4096) return fail(MSA_ERR_INVALID_ARG, "B must be in [1, 4096] (got %d)", B);
+  if (M < 1 || M > kTreeMaxDrafts) return fail(MSA_ERR_INVALID_ARG, "M must be in [1, %d] (got %d)", kTreeMaxDrafts, M);
+  if (t_loc_max < 0) return fail(MSA_ERR_INVALID_ARG, "t_loc_max must be >= 0 (got %d)", t_loc_max);
+  if (k < 0 || k > 256) return fail(MSA_ERR_INVALID_ARG, "k must be in [0, 256] (got %d)", k);
+  if (!(softmax_scale >= 0.f) || !std::isfinite(softmax_scale))
+    return fail(MSA_ERR_INVALID_ARG, "softmax_scale must be finite and >= 0");
+  CHECK_PTR(q);
+  CHECK_PTR(K_draft);
+  CHECK_PTR(V_draft);
+  CHECK_PTR(mask);
+  CHECK_OPT_PTR(n_draft);
+  CHECK_PTR(loc_len);
+  CHECK_PTR(out);
+  if (t_loc_max > 0) {
+    CHECK_PTR(K_loc);
+    CHECK_PTR(V_loc);
+  }
+  if (k > 0) {
+    if (n_docs < 1 || n_chunks < n_docs)
+      return fail(MSA_ERR_INVALID_ARG, "need 1 <= n_docs <= n_chunks (got %d, %d)", n_docs, n_chunks);
+    if (k > n_docs) return fail(MSA_ERR_INVALID_ARG, "k must be <= n_docs (got %d, %d)", k, n_docs);
+    CHECK_PTR(K_bar);
+    CHECK_PTR(V_bar);
+    CHECK_PTR(chunk_off);
+    CHECK_PTR(topk_idx);
+  }
+  const size_t need = tree_attend_workspace(*dims, B, M, k, t_loc_max);
+  if (ws_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  if (need && (!ws || misaligned(ws, 256)))
+    return fail(MSA_ERR_INVALID_ARG, "workspace must be non-NULL and 256-byte aligned");
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  TreeAttendCall c{q,     K_draft, V_draft, mask,   n_draft,  B,        M, K_loc,         V_loc, loc_len, t_loc_max,
+                   K_bar, V_bar,   chunk_off, n_docs, n_chunks, topk_idx, k, softmax_scale, out,   ws};
+  return tree_attend_launch(*dims, c, static_cast<cudaStream_t>(stream));
+}
+
+msa_status msa_tree_commit(const msa_dims* dims, const void* K_draft, const void* V_draft, const int32_t* path,
+                           const int32_t* n_path, int32_t B, int32_t M, int32_t A, void* K_loc, void* V_loc,
+                           const int32_t* loc_len, int32_t t_loc_max, int32_t* new_len, void* stream) {
+  CHECK_STATUS(check_dims(dims, true, false));
+  if (B < 1 || B > 65535) return fail(MSA_ERR_INVALID_ARG, "B must be in [1, 65535] (got %d)", B);
+  if (M < 1 || M > kTreeMaxDrafts) return fail(MSA_ERR_INVALID_ARG, "M must be in [1, %d] (got %d)", kTreeMaxDrafts, M);
+  if (A < 1 || A > M) return fail(MSA_ERR_INVALID_ARG, "A must be in [1, M] (got %d, M %d)", A, M);
+  if (t_loc_max < 1) return fail(MSA_ERR_INVALID_ARG, "t_loc_max must be >= 1 (got %d)", t_loc_max);
+  CHECK_PTR(K_draft);
+  CHECK_PTR(V_draft);
+  CHECK_PTR(path);
+  CHECK_PTR(n_path);
+  CHECK_PTR(K_loc);
+  CHECK_PTR(V_loc);
+  CHECK_PTR(loc_len);
+  CHECK_PTR(new_len);
+  if (new_len == loc_len) return fail(MSA_ERR_INVALID_ARG, "new_len must not be loc_len");
+  if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
+  return tree_commit_launch(*dims, K_draft, V_draft, path, n_path, B, M, A, K_loc, V_loc, loc_len, t_loc_max, new_len,
+                            static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------ tracing ------------------------------
