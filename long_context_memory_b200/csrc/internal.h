@@ -111,6 +111,11 @@ msa_status encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int ra
                              const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
                              CUtensorMapSwizzle swizzle);
 
+// the same without the memory of earlier calls
+msa_status encode_tensor_map_once(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* gaddr,
+                                  const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                                  CUtensorMapSwizzle swizzle);
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // theta_i / (2 pi) as 64-bit binary fractions, theta_i = base^(-2i/head_dim) (computed in long double)

@@ -212,6 +212,19 @@ msa_status encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, int ra
   return MSA_OK;
 }
 
+msa_status encode_tensor_map_once(CUtensorMap* map, CUtensorMapDataType dtype, int rank, const void* gaddr,
+                                  const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box,
+                                  CUtensorMapSwizzle swizzle) {
+  auto fn = get_encoder();
+  if (!fn) return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
+  const uint32_t elem_strides[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(map, dtype, rank, const_cast<void*>(gaddr), dims, strides_bytes, box, elem_strides,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", (int)r);
+  return MSA_OK;
+}
+
 // ---------------------------------------------------------------------------
 // tracing
 // ---------------------------------------------------------------------------
