@@ -138,6 +138,18 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort));
 }
 
+// The same waits for short dependency chains (a few hundred cycles from one warp to the next): the
+// clock, whose read costs more than such a wait, is looked at only after a number of tries.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort);
+}
+__device__ __forceinline__ bool warp_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  return __all_sync(0xffffffffu, mbar_wait_short(bar, parity, abort));
+}
+
 // Named barrier among `nthreads` threads that also returns whether any of them passed `pred`
 // (bar.red.or): a group of warps that must stay in step (their named barriers have no time
 // limit) decides together whether to leave its loop.

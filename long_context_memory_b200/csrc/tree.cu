@@ -126,18 +126,20 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // 2^kSlack (O is then rescaled in tensor memory; weights stay below 2^kSlack otherwise, far
 // inside bf16's and fp32's range), so that a tile normally touches O in the MMA alone.
 //
-// Keys of a query: its documents' pooled rows in groups of 8 (each document padded to whole
-// groups), 16 groups to a tile; the local rows; the drafts.  Work is cut evenly: all tiles of all
-// (query, row block, KV head) items in one line, CTA c of N takes tiles c W / N .. (c + 1) W / N, so
-// (N = the SMs, or W where there are fewer tiles), so ragged batches and single long queries fill
-// the GPU alike; the at most two items that a CTA
-// shares with its neighbours leave partial results that tree_combine_kernel merges.
+// Keys of a query: its documents' pooled rows one after the other, the local rows, the drafts, each
+// in tiles of 128.  Work is cut evenly: all tiles of all (query, row block, KV head) items in one
+// line, CTA c of N takes tiles c W / N .. (c + 1) W / N (N = the SMs, or W where there are fewer
+// tiles), so ragged batches and single long queries fill the GPU alike; the at most two items that a
+// CTA shares with its neighbours leave partial results and a note for tree_combine_kernel, which
+// merges them.
 //
-// Only value rows that some draft sees are copied (boxes of 128 and 8 rows, and single rows in
-// 16-byte pieces where a group of 8 is not whole), into a ring whose V slots start as zeros where
-// a first copy does not fill them: whatever stands in the rows behind a sequence, and in drafts
-// that nobody sees, never reaches a product.  (Keys come in whole groups: a score that a row does
-// not see is replaced, not multiplied.)
+// A tile's rows arrive by TMA boxes of 128, 32, 8 and 1 rows.  A box costs the TMA unit about 55
+// cycles and 2.3 per row of 128 bytes (measured), so a run of rows is covered by equal boxes whose
+// last one overlaps the one before (the same bytes twice) rather than by ever smaller ones; a box
+// may start at any row of the tile, since the 128-byte swizzle goes by the address.  Only rows that
+// some draft sees are copied, into a ring whose V slots start as zeros where a first copy does not
+// fill them: whatever stands in the rows behind a sequence, and in drafts that nobody sees, never
+// reaches a product.
 //
 // Warps: 4 NT softmax warps (a thread per row), one producer (item headers, document tables, TMA),
 // one MMA issuer.  One CTA per SM (its ring fills the shared memory).
@@ -148,25 +150,26 @@ constexpr int kSmallB = 64;       // queries whose tile counts every CTA compute
 constexpr float kSlack = 8.f;
 constexpr int kTmemCols = 512;    // scores 2 x 128, outputs 2 x 128
 
+constexpr int kBoxRows[4] = {1, 8, 32, 128};
+
 struct TreeMaps {
   CUtensorMap q;
-  CUtensorMap kl128, vl128;               // local cache, 128 rows
-  CUtensorMap kl8, vl8, kd8, vd8, kb8, vb8;  // local cache, drafts, pooled rows: 8 rows
+  // [K, V][box rows]: kBoxRows for the pooled rows and the local cache, 1 and 8 rows of drafts
+  CUtensorMap bar[2][3], loc[2][4], draft[2][2];
 };
 
 struct TreeP {
   const int32_t *mask, *n_draft, *loc_len, *chunk_off, *topk_idx;
-  const __nv_bfloat16 *V_draft, *V_loc, *V_bar;
   __nv_bfloat16* out;
-  int64_t* prefix;   // [B + 1] tiles before each query's first
-  int32_t* groups;   // [B] pooled 8-row groups of each query (B > kSmallB)
-  float* part_o;     // [2 N][NT * 128][D] unnormalised
+  int4* merges;      // [N][2] item cut by CTA c's begin: query, first draft, KV head, drafts | first and last CTA, first part's slot
+  int32_t* sel;      // [B] pooled rows of each query's documents (B > kSmallB)
+  float* part_o;     // [2 N][D / 4][NT * 128][4] unnormalised (a warp's rows side by side)
   float* part_ml;    // [2 N][NT * 128][2] reference maximum, sum
   int B, M, W, n_q, n_kv, G, TT, n_rb, t_loc_max, n_docs, n_chunks, k, ring;
   float scale_log2;
 };
 
-enum { kHb = 0, kHt0, kHhk, kHL, kHn, kHNg, kHTc, kHTl, kHlo, kHhi, kHtab, kHslot, kHWords = 16 };
+enum { kHb = 0, kHt0, kHhk, kHsel, kHL, kHn, kHTc, kHTl, kHlo, kHhi, kHslot, kHWords = 16 };
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -181,8 +184,8 @@ __device__ __forceinline__ int drafts_of(const TreeP& p, int b) {
   return p.n_draft ? max(0, min(p.n_draft[b], p.M)) : p.M;
 }
 __device__ __forceinline__ int local_of(const TreeP& p, int b) { return max(0, min(p.loc_len[b], p.t_loc_max)); }
-__device__ __forceinline__ int tiles_of(int groups, int L, int n) {
-  return (groups + 15) / 16 + (L + kTile - 1) / kTile + (n + kTile - 1) / kTile;
+__device__ __forceinline__ int tiles_of(int sel, int L, int n) {
+  return (sel + kTile - 1) / kTile + (L + kTile - 1) / kTile + (n + kTile - 1) / kTile;
 }
 // row blocks of a query that hold a draft in use
 template <int NT>
@@ -190,48 +193,120 @@ __device__ __forceinline__ int blocks_of(const TreeP& p, int n) {
   return (n + NT * p.TT - 1) / (NT * p.TT);
 }
 
-// scores that the row does not see become -inf; the largest of the rest
-__device__ __forceinline__ float hide_and_max(float (&s)[32], uint32_t see, bool all) {
-  if (!all) {
-    asm volatile("" : "+r"(see));  // a branch of its own, its tests made where they are used
+__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// scores that the row does not see become -inf
+__device__ __forceinline__ void hide(float (&s)[32], uint32_t see) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
-      if (!(see >> e & 1)) s[e] = -INFINITY;
-  }
-  float m[4] = {s[0], s[1], s[2], s[3]};
+  for (int e = 0; e < 32; ++e)
+    if (!(see >> e & 1)) s[e] = -INFINITY;
+}
+__device__ __forceinline__ float max_of(const float (&s)[32], float m0) {
+  float m[4] = {fmaxf(s[0], m0), s[1], s[2], s[3]};
 #pragma unroll
   for (int e = 4; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], s[e]);
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
-// weights 2^(s c + neg) of 32 keys to tensor memory as bf16 pairs; returns their sum
-__device__ __forceinline__ float weigh_quarter(const float (&s)[32], float c, float neg, uint32_t addr) {
-  uint32_t u[16];
-  float sum[4] = {0.f, 0.f, 0.f, 0.f};
+// Largest of the tile's 128 scores of this row (quarters of 32 keys; two loads in flight).
+template <bool MASKED>
+__device__ __forceinline__ float row_max(uint32_t addr, const uint32_t (&see)[4]) {
+  float sa[32], sb[32];
+  float m = -INFINITY;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const float a = ex2(fmaf(s[2 * e], c, neg)), z = ex2(fmaf(s[2 * e + 1], c, neg));
-    sum[e & 3] += a + z;
-    u[e] = pack_bf16x2(a, z);
+  for (int q = 0; q < 4; q += 2) {
+    tmem_ld32(addr + 32 * q, sa);
+    tmem_ld32(addr + 32 * q + 32, sb);
+    tmem_ld_wait_for(sa);
+    tmem_ld_wait_for(sb);
+    if (MASKED) {
+      hide(sa, see[q]);
+      hide(sb, see[q + 1]);
+    }
+    m = max_of(sa, m);
+    m = max_of(sb, m);
   }
-  tmem_st16(addr, u);
-  return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  return m;
 }
 
-// each query's pooled groups (large batches only): a warp per query
-__global__ void __launch_bounds__(256) tree_groups_kernel(const int32_t* __restrict__ topk_idx,
+// The scores again, a quarter at a time with the next one's load in flight: weights 2^(s c + neg) as
+// bf16 pairs over the columns of quarters already read; returns their fp32 sum.
+template <bool MASKED>
+__device__ __forceinline__ float row_weights(uint32_t addr, const uint32_t (&see)[4], float c, float neg) {
+  float sa[32], sb[32];
+  const uint64_t c2 = pack_f32x2(c, c), neg2 = pack_f32x2(neg, neg);
+  uint64_t sum[2] = {0, 0};  // two pairs of fp32 zeros
+  tmem_ld32(addr, sa);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float(&cur)[32] = q & 1 ? sb : sa;
+    tmem_ld_wait_for(cur);
+    if (q < 3) tmem_ld32(addr + 32 * (q + 1), q & 1 ? sa : sb);
+    if (MASKED) hide(cur, see[q]);
+    uint32_t u[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint64_t y = fma_f32x2(pack_f32x2(cur[2 * e], cur[2 * e + 1]), c2, neg2);
+      const float a = ex2(__uint_as_float((uint32_t)y)), z = ex2(__uint_as_float((uint32_t)(y >> 32)));
+      sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(a, z));
+      u[e] = pack_bf16x2(a, z);
+    }
+    tmem_st16(addr + 16 * q, u);
+  }
+  sum[0] = add_f32x2(sum[0], sum[1]);
+  return __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
+}
+
+// each query's pooled rows (large batches only): a warp per query
+__global__ void __launch_bounds__(256) tree_select_kernel(const int32_t* __restrict__ topk_idx,
                                                           const int32_t* __restrict__ chunk_off, int B, int k,
-                                                          int n_docs, int n_chunks, int32_t* __restrict__ groups) {
+                                                          int n_docs, int n_chunks, int32_t* __restrict__ sel) {
   pdl_enter();
   const int b = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (b >= B) return;
   int g = 0;
   for (int r = lane; r < k; r += 32) {
     const int doc = topk_idx[(size_t)b * k + r];
-    if (doc >= 0 && doc < n_docs) g += (max(0, min(chunk_off[doc + 1] - chunk_off[doc], n_chunks)) + 7) / 8;
+    if (doc >= 0 && doc < n_docs) g += max(0, min(chunk_off[doc + 1] - chunk_off[doc], n_chunks));
   }
   g = __reduce_add_sync(0xffffffffu, g);
-  if (lane == 0) groups[b] = g;
+  if (lane == 0) sel[b] = g;
+}
+
+// floor(a b / c) for a b < 2^63, with 32-bit arithmetic where it fits
+__device__ __forceinline__ long long muldiv(long long a, int b, int c) {
+  const long long ab = a * b;
+  return ab >> 32 ? ab / c : (long long)((uint32_t)ab / (uint32_t)c);
+}
+__device__ __forceinline__ int divide(long long a, long long b) {  // floor(a / b), the result an int
+  return (a | b) >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
+}
+
+// boxes that cover a run of n rows: of the largest size (1, 8, 32) that is not longer than the run,
+// the last one moved back to end with it
+struct Cover {
+  int size, count, level;
+};
+__device__ __forceinline__ Cover cover_of(int n) {
+  Cover c;
+  c.level = n >= 32 ? 2 : n >= 8 ? 1 : 0;
+  c.size = n >= 32 ? 32 : n >= 8 ? 8 : 1;
+  c.count = (n + c.size - 1) / c.size;
+  return c;
 }
 
 template <int D, int NT>
@@ -248,7 +323,7 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
   __shared__ uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
   __shared__ uint64_t qfull, qempty, sfull[2], pready[2], pvdone[2], ofree[2], hfull[2], hempty[2], drained;
   __shared__ int hdr[2][kHWords];
-  __shared__ int cnt[kSmallB];
+  __shared__ int q_sel[kSmallB], q_loc[kSmallB], q_n[kSmallB];  // small batches: pooled rows, local rows, drafts
   __shared__ long long warp_sum[kThreads / 32];
   __shared__ long long first_base;
   __shared__ int first_b;
@@ -258,7 +333,7 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
   uint8_t* qs = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);  // [NT] row tiles (swizzle atoms: 1 KB aligned)
   uint8_t* ks = qs + NT * kTB;            // [ring] key tiles
   uint8_t* vs = ks + p.ring * kTB;        // [ring] value tiles
-  int* tab = reinterpret_cast<int*>(vs + p.ring * kTB);  // [2][2][k + 1]: first group * 8 + rows % 8; first row
+  int* tab = reinterpret_cast<int*>(vs + p.ring * kTB);  // the query's documents: [k + 1] first key, [k] first row
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -287,29 +362,48 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     tmem_alloc(&tmem_slot, kTmemCols);
     tmem_relinquish();
   }
-  for (int i = tid; i < kSmallB; i += kThreads) cnt[i] = 0;
+  for (int i = tid; i < kSmallB; i += kThreads) q_sel[i] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   pdl_enter();
 
-  // ---- the line of tiles: every CTA counts it, CTA 0 leaves it for the merge ----
+  // ---- the line of tiles: every CTA counts it (small batches: with everything in shared memory) ----
   const bool small = p.B <= kSmallB;
-  if (small && p.k) {
-    for (int i = tid; i < p.B * p.k; i += kThreads) {
-      const int doc = p.topk_idx[i];
-      if (doc >= 0 && doc < p.n_docs)
-        atomicAdd(&cnt[i / p.k], (doc_rows(p, doc) + 7) / 8);
-      else
-        raise_dev_error(kDevErrBadIndex);
+  if (small) {
+    if (tid < p.B) {
+      q_n[tid] = drafts_of(p, tid);
+      q_loc[tid] = local_of(p, tid);
+    }
+    const int pairs = p.B * p.k;
+    for (int i0 = tid; i0 < pairs; i0 += 4 * kThreads) {  // four documents of a thread in flight
+      int rows[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = i0 + u * kThreads;
+        rows[u] = -1;
+        if (i < pairs) {
+          const int doc = p.topk_idx[i];
+          if (doc >= 0 && doc < p.n_docs) rows[u] = doc_rows(p, doc);
+          else raise_dev_error(kDevErrBadIndex);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (rows[u] > 0) atomicAdd(&q_sel[(i0 + u * kThreads) / p.k], rows[u]);
     }
     __syncthreads();
   }
+  auto query = [&](int b, int& sel, int& L, int& n) {
+    n = small ? q_n[b] : drafts_of(p, b);
+    L = small ? q_loc[b] : local_of(p, b);
+    sel = small ? q_sel[b] : p.k ? p.sel[b] : 0;
+  };
   auto cost_of = [&](int b) -> long long {
-    const int n = drafts_of(p, b);
-    const int g = p.k ? (small ? cnt[b] : p.groups[b]) : 0;
-    return (long long)p.n_kv * blocks_of<NT>(p, n) * tiles_of(g, local_of(p, b), n);
+    int sel, L, n;
+    query(b, sel, L, n);
+    return (long long)p.n_kv * blocks_of<NT>(p, n) * tiles_of(sel, L, n);
   };
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -329,36 +423,38 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     if (w < warp) base += warp_sum[w];
     total += warp_sum[w];
   }
-  const long long n_act = max(1ll, min((long long)gridDim.x, total));  // CTAs with work
-  const long long w_begin = min(total, total * blockIdx.x / n_act), w_end = min(total, total * (blockIdx.x + 1) / n_act);
-  for (int b = b0; b < b1; ++b) {
+  // CTA c of the n_act with work begins at tile floor(c total / n_act)
+  const int n_act = (int)max(1ll, min((long long)gridDim.x, total));
+  auto begin_of = [&](int c) { return min(total, muldiv(total, c, n_act)); };
+  const long long w_begin = begin_of(blockIdx.x), w_end = begin_of(blockIdx.x + 1);
+  for (int b = b0; b < b1 && w_begin < w_end; ++b) {
     const long long c = cost_of(b);
-    if (blockIdx.x == 0) p.prefix[b] = base;
-    if (w_begin < w_end && base <= w_begin && w_begin < base + c) {
+    if (base <= w_begin && w_begin < base + c) {
       first_b = b;
       first_base = base;
     }
     base += c;
   }
-  if (blockIdx.x == 0 && tid == 0) p.prefix[p.B] = total;
   __syncthreads();
 
   if (warp == kSoftWarps) {
     // =======================================================================
     // producer
     // =======================================================================
-    uint32_t x = 0;  // tiles loaded
-    int n_items = 0, tb = 0;
+    uint32_t x = 0;     // tiles loaded
+    int st = 0, ph = 1;  // ring slot of tile x; parity of the phase in which that slot was emptied last
+    int n_items = 0;
     bool ok = true;
     long long w = w_begin;
     long long bbase = first_base;
     int b = first_b;
-    bool fresh = true;  // b's table is still to be built
-    int L = 0, n = 0, Ng = 0;
-    const int tstride = p.k + 1;
+    bool fresh = true, listed = false;  // b is new; its documents are in the table
+    int L = 0, n = 0, sel = 0, T = 0;
+    int *first_key = tab, *first_row = tab + p.k + 1;
+    if (lane == 0) p.merges[2 * blockIdx.x].x = -1;
     while (ok) {
       const int hb = n_items & 1;
-      if (n_items >= 2 && !warp_wait(&hempty[hb], ((n_items >> 1) - 1) & 1, &abort_flag)) {
+      if (n_items >= 2 && !warp_wait_short(&hempty[hb], ((n_items >> 1) - 1) & 1, &abort_flag)) {
         ok = false;
         break;
       }
@@ -370,31 +466,84 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
         }
         break;
       }
-      int T = 0;
       for (;;) {
         if (fresh) {
-          n = drafts_of(p, b);
-          L = local_of(p, b);
-          Ng = 0;
-          if (p.k) {
-            tb ^= 1;
-            int* tp = tab + tb * 2 * tstride;
+          query(b, sel, L, n);
+          T = tiles_of(sel, L, n);
+          fresh = listed = false;
+        }
+        const long long c = (long long)p.n_kv * blocks_of<NT>(p, n) * T;
+        if (w < bbase + c) break;
+        bbase += c;
+        ++b;
+        fresh = true;
+      }
+      const int item = divide(w - bbase, T), lo = (int)(w - bbase - (long long)item * T);
+      const int hi = (int)min((long long)T, lo + (w_end - w));
+      const int rb = item / p.n_kv, hk = item - rb * p.n_kv;
+      const int t0 = rb * NT * p.TT;
+      const int Tc = (sel + kTile - 1) / kTile, Tl = (L + kTile - 1) / kTile;
+      if (lane == 0) {
+        h[kHb] = b;
+        h[kHt0] = t0;
+        h[kHhk] = hk;
+        h[kHsel] = sel;
+        h[kHL] = L;
+        h[kHn] = n;
+        h[kHTc] = Tc;
+        h[kHTl] = Tl;
+        h[kHlo] = lo;
+        h[kHhi] = hi;
+        // whole items are written out; a shared one leaves its part: slot 0 of the CTA's first item, 1 of its last
+        h[kHslot] = (lo == 0 && hi == T) ? -1 : 2 * (int)blockIdx.x + (n_items > 0);
+        mbar_arrive(&hfull[hb]);
+      }
+      // queries: NT row tiles of TT drafts x G heads
+      if (n_items >= 1 && !warp_wait_short(&qempty, (n_items - 1) & 1, &abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&qfull, NT * DB * p.G * p.TT * 128);
+        for (int i = 0; i < NT; ++i)
+          for (int d = 0; d < DB; ++d)
+            tma_load_4d(qs + i * kTB + d * kBlk, &maps.q, &qfull, d * 64, hk * p.G, t0 + i * p.TT, b);
+      }
+      if (lo > 0 && n_items == 0 && lane == 0) {
+        // the item began in an earlier CTA: the first CTA that it reaches notes it for the merge
+        const long long w0 = w - lo;  // tile w is in the CTA floor(((w + 1) N - 1) / W)
+        const int ca = divide((w0 + 1) * n_act - 1, total), cz = divide((w0 + T) * n_act - 1, total);
+        if (ca + 1 == (int)blockIdx.x) {
+          p.merges[2 * blockIdx.x + 1] = make_int4(ca, cz, 2 * ca + (begin_of(ca) == w0 ? 0 : 1), 0);
+          p.merges[2 * blockIdx.x] = make_int4(b, t0, hk, n);
+        }
+      }
+      ++n_items;
+      for (int t = lo; t < hi && ok; ++t, ++x) {
+        const int c0 = t * kTile, j0 = (t - Tc) * kTile, d0 = (t - Tc - Tl) * kTile;
+        const int kind = t < Tc ? 0 : t < Tc + Tl ? 1 : 2;  // pooled rows, local rows, drafts
+        int rows, boxed;         // rows that the tile holds; rows that its boxes bring
+        int doc0 = 0;            // kind 0: the first document with keys in the tile
+        uint32_t bits = 0;       // kind 2, lane < 16: drafts d0 + 8 lane .. that some draft of the query sees
+        if (kind == 0) {
+          if (!listed) {  // the query's documents: first key (a running sum) and first pooled row of each
             const int each = (p.k + 31) / 32;
             int sum = 0;
+            __syncwarp();
             for (int q = 0; q < each; ++q) {
               const int r = lane * each + q;
               if (r < p.k) {
                 const int doc = p.topk_idx[(size_t)b * p.k + r];
-                int rows = 0, row0 = 0;
+                int n_rows = 0, row0 = 0;
                 if (doc >= 0 && doc < p.n_docs) {
-                  rows = doc_rows(p, doc);
+                  n_rows = doc_rows(p, doc);
                   row0 = p.chunk_off[doc];
                 } else {
                   raise_dev_error(kDevErrBadIndex);
                 }
-                tp[r] = rows;
-                tp[tstride + r] = row0;
-                sum += (rows + 7) / 8;
+                first_key[r] = n_rows;
+                first_row[r] = row0;
+                sum += n_rows;
               }
             }
             int in = sum;
@@ -407,156 +556,100 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
             for (int q = 0; q < each; ++q) {
               const int r = lane * each + q;
               if (r < p.k) {
-                const int rows = tp[r];
-                tp[r] = run * 8 + (rows & 7);
-                run += (rows + 7) / 8;
+                const int n_rows = first_key[r];
+                first_key[r] = run;
+                run += n_rows;
               }
             }
-            Ng = __shfl_sync(0xffffffffu, in, 31);
-            if (lane == 0) tp[p.k] = Ng * 8;
+            if (lane == 0) first_key[p.k] = sel;
+            listed = true;
             __syncwarp();
           }
-          fresh = false;
-        }
-        T = tiles_of(Ng, L, n);
-        const long long c = (long long)p.n_kv * blocks_of<NT>(p, n) * T;
-        if (w < bbase + c) break;
-        bbase += c;
-        ++b;
-        fresh = true;
-      }
-      const long long off = w - bbase;
-      const int item = (int)(off / T), lo = (int)(off - (long long)item * T);
-      const int hi = (int)min((long long)T, lo + (w_end - w));
-      const int rb = item / p.n_kv, hk = item - rb * p.n_kv;
-      const int t0 = rb * NT * p.TT;
-      const int Tc = (Ng + 15) / 16, Tl = (L + kTile - 1) / kTile;
-      if (lane == 0) {
-        h[kHb] = b;
-        h[kHt0] = t0;
-        h[kHhk] = hk;
-        h[kHL] = L;
-        h[kHn] = n;
-        h[kHNg] = Ng;
-        h[kHTc] = Tc;
-        h[kHTl] = Tl;
-        h[kHlo] = lo;
-        h[kHhi] = hi;
-        h[kHtab] = tb;
-        // whole items are written out; a shared one leaves its part: slot 0 of the CTA's first item, 1 of its last
-        h[kHslot] = (lo == 0 && hi == T) ? -1 : 2 * (int)blockIdx.x + (n_items > 0);
-        mbar_arrive(&hfull[hb]);
-      }
-      // queries: NT row tiles of TT drafts x G heads
-      if (n_items >= 1 && !warp_wait(&qempty, (n_items - 1) & 1, &abort_flag)) {
-        ok = false;
-        break;
-      }
-      if (lane == 0) {
-        mbar_arrive_expect_tx(&qfull, NT * DB * p.G * p.TT * 128);
-        for (int i = 0; i < NT; ++i)
-          for (int d = 0; d < DB; ++d)
-            tma_load_4d(qs + i * kTB + d * kBlk, &maps.q, &qfull, d * 64, hk * p.G, t0 + i * p.TT, b);
-      }
-      ++n_items;
-      const int* tp = tab + tb * 2 * tstride;
-      for (int t = lo; t < hi && ok; ++t, ++x) {
-        const uint32_t st = x % p.ring, ph = (x / p.ring - 1) & 1;
-        // the tile as 16 groups of 8 rows: lane < 16 holds its group's first row and the rows to copy
-        const CUtensorMap *mk8, *mv8;
-        const __nv_bfloat16* vsrc;  // the value rows' tensor at row 0 of this query
-        int g_row = 0;
-        uint32_t g_bits = 0;
-        bool full = false;  // 128 consecutive rows: one box
-        const int j0 = (t - Tc) * kTile, d0 = (t - Tc - Tl) * kTile;
-        if (t < Tc) {
-          mk8 = &maps.kb8;
-          mv8 = &maps.vb8;
-          vsrc = p.V_bar;
-          const int g = t * 16 + lane;
-          if (lane < 16 && g < Ng) {
-            int a = 0, z = p.k - 1;  // the last document whose first group is at or before g
-            while (a < z) {
-              const int mid = (a + z + 1) >> 1;
-              if ((tp[mid] >> 3) <= g) a = mid; else z = mid - 1;
-            }
-            const int g0 = tp[a] >> 3, g1 = tp[a + 1] >> 3, rest = tp[a] & 7;
-            g_row = tp[tstride + a] + (g - g0) * 8;
-            g_bits = g == g1 - 1 && rest ? (1u << rest) - 1 : 0xFFu;
+          rows = min(kTile, sel - c0);
+          int z = p.k - 1;
+          while (doc0 < z) {
+            const int mid = (doc0 + z + 1) >> 1;
+            if (first_key[mid] <= c0) doc0 = mid; else z = mid - 1;
           }
-        } else if (t < Tc + Tl) {
-          mk8 = &maps.kl8;
-          mv8 = &maps.vl8;
-          vsrc = p.V_loc + (size_t)b * p.t_loc_max * p.n_kv * D;
-          full = L - j0 >= kTile;
-          g_row = j0 + 8 * lane;
-          if (lane < 16) g_bits = (1u << max(0, min(8, L - g_row))) - 1;
+          boxed = 0;
+          for (int r = doc0 + lane; r < p.k && first_key[r] < c0 + rows; r += 32) {
+            const int run = min(first_key[r + 1], c0 + rows) - max(first_key[r], c0);
+            const Cover c = cover_of(max(run, 0));
+            boxed += c.size * c.count;
+          }
+          boxed = __reduce_add_sync(0xffffffffu, boxed);
+        } else if (kind == 1) {
+          rows = min(kTile, L - j0);
+          const Cover c = cover_of(rows);
+          boxed = rows == kTile ? kTile : c.size * c.count;
         } else {
-          mk8 = &maps.kd8;
-          mv8 = &maps.vd8;
-          vsrc = p.V_draft + (size_t)b * p.M * p.n_kv * D;
-          g_row = d0 + 8 * lane;
-          uint32_t seen[4] = {0, 0, 0, 0};  // drafts that some draft of the query sees
+          uint32_t seen[4] = {0, 0, 0, 0};
           for (int r = lane; r < n; r += 32) {
             const int32_t* mk = p.mask + ((size_t)b * p.M + r) * p.W + d0 / 32;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (d0 / 32 + q < p.W) seen[q] |= (uint32_t)mk[q];
           }
+          rows = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             seen[q] = __reduce_or_sync(0xffffffffu, seen[q]);
             const int left = n - d0 - 32 * q;
             if (left < 32) seen[q] &= left > 0 ? (1u << left) - 1 : 0u;
-            g_bits |= (lane >> 2) == q ? seen[q] >> (8 * (lane & 3)) & 0xFFu : 0u;
+            bits |= (lane >> 2) == q ? seen[q] >> (8 * (lane & 3)) & 0xFFu : 0u;
+            rows += __popc(seen[q]);
           }
+          boxed = rows;
         }
-        const int n_rows = __reduce_add_sync(0xffffffffu, __popc(g_bits));
-        const uint32_t broken = __ballot_sync(0xffffffffu, g_bits != 0 && g_bits != 0xFFu);
-        const int n_groups = __popc(__ballot_sync(0xffffffffu, g_bits != 0));
         for (int kv = 0; kv < 2; ++kv) {
           uint64_t* fullb = (kv ? vfull : kfull) + st;
           uint8_t* dst = (kv ? vs : ks) + st * kTB;
-          if (x >= (uint32_t)p.ring && !warp_wait((kv ? vempty : kempty) + st, ph, &abort_flag)) {
+          if (x >= (uint32_t)p.ring && !warp_wait_short((kv ? vempty : kempty) + st, ph, &abort_flag)) {
             ok = false;
             break;
           }
-          if (kv && x < (uint32_t)p.ring && n_rows < kTile) {  // a slot's first use that leaves rows out
+          if (kv && x < (uint32_t)p.ring && rows < kTile) {  // a slot's first use that leaves rows out
             for (int i = lane; i < kTB / 16; i += 32) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive_expect_tx(fullb, (kv ? n_rows : 8 * n_groups) * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(fullb, boxed * D * 2);
           __syncwarp();
-          if (full) {
-            if (lane < DB)
-              tma_load_4d(dst + lane * kBlk, kv ? &maps.vl128 : &maps.kl128, fullb, lane * 64, hk, j0, b);
-          } else {
-            if (kv ? g_bits == 0xFFu : g_bits != 0) {
-              const CUtensorMap* m = kv ? mv8 : mk8;
-              for (int d = 0; d < DB; ++d) {
-                uint8_t* to = dst + d * kBlk + lane * 1024;
-                if (t < Tc)
-                  tma_load_3d(to, m, fullb, d * 64, hk, g_row);
-                else
-                  tma_load_4d(to, m, fullb, d * 64, hk, g_row, b);
+          if (kind == 0) {
+            for (int r = doc0 + lane; r < p.k && first_key[r] < c0 + rows; r += 32) {
+              const int a = max(first_key[r], c0), run = min(first_key[r + 1], c0 + rows) - a;
+              if (run <= 0) continue;
+              const Cover c = cover_of(run);
+              const int src = first_row[r] + (a - first_key[r]);
+              for (int i = 0; i < c.count; ++i) {
+                const int o = min(i * c.size, run - c.size);
+                for (int d = 0; d < DB; ++d)
+                  tma_load_3d(dst + d * kBlk + (a - c0 + o) * 128, &maps.bar[kv][c.level], fullb, d * 64, hk, src + o);
               }
             }
-            for (uint32_t left = kv ? broken : 0u; left; left &= left - 1) {
-              const int src = __ffs(left) - 1;
-              const uint32_t bits = __shfl_sync(0xffffffffu, g_bits, src);
-              const int row = __shfl_sync(0xffffffffu, g_row, src);
-              const __nv_bfloat16* from = vsrc + ((size_t)row * p.n_kv + hk) * D;
-#pragma unroll
-              for (int u = lane; u < 64 * DB; u += 32) {  // 8 rows x 8 DB pieces, at their swizzled places
-                const int r = u / (8 * DB), c = u % (8 * DB);
-                if (bits >> r & 1)
-                  bulk_load(dst + (c >> 3) * kBlk + (src * 8 + r) * 128 + (((c & 7) ^ r) << 4),
-                            from + (size_t)r * p.n_kv * D + c * 8, 16, fullb);
-              }
+          } else if (kind == 1) {
+            const bool whole = rows == kTile;
+            const Cover c = cover_of(rows);
+            const int count = whole ? 1 : c.count;
+            if (lane < count * DB) {
+              const int i = lane / DB, d = lane % DB, o = whole ? 0 : min(i * c.size, rows - c.size);
+              tma_load_4d(dst + d * kBlk + o * 128, &maps.loc[kv][whole ? 3 : c.level], fullb, d * 64, hk, j0 + o, b);
+            }
+          } else {
+            for (int d = 0; d < DB; ++d) {
+              uint8_t* to = dst + d * kBlk + lane * 1024;
+              if (bits == 0xFFu)
+                tma_load_4d(to, &maps.draft[kv][1], fullb, d * 64, hk, d0 + 8 * lane, b);
+              else
+                for (int r = 0; r < 8; ++r)
+                  if (bits >> r & 1) tma_load_4d(to + r * 128, &maps.draft[kv][0], fullb, d * 64, hk, d0 + 8 * lane + r, b);
             }
           }
           __syncwarp();
+        }
+        if (++st == p.ring) {
+          st = 0;
+          ph ^= 1;
         }
       }
       w += hi - lo;
@@ -574,54 +667,67 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     if (lane == 0) {
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128);
       constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | kIdescBMnMajor;
-      const uint32_t qa = smem_u32(qs), ka = smem_u32(ks), va = smem_u32(vs);
+      const uint64_t qd = umma_desc_k_sw128(smem_u32(qs)), kd = umma_desc_k_sw128(smem_u32(ks)),
+                     vd = umma_desc_mn_sw128(smem_u32(vs), kBlk);
+      // ring places of the next key tile to multiply with Q and of the next value tile (slot, parity)
+      int ks_st = 0, ks_ph = 0, vs_st = 0, vs_ph = 0;
       uint32_t x = 0;
       bool ok = true;
-      auto scores = [&](int i, uint32_t xx, bool last_reader) {  // S of row tile i and key tile xx
-        const uint32_t st = xx % p.ring;
-        if (!mbar_wait(&kfull[st], (xx / p.ring) & 1, &abort_flag)) return false;
+      auto scores = [&](int i, uint32_t xx) {  // S of row tile i and key tile xx
+        if (i == 0 && !mbar_wait_short(&kfull[ks_st], ks_ph, &abort_flag)) return false;
         tc_fence_after();
         const uint32_t slot = NT == 1 ? (xx & 1) : i;
+        const uint64_t a = qd + (uint64_t)(i * kTB / 16), k = kd + (uint64_t)(ks_st * (kTB / 16));
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
-          const uint32_t o = (s >> 2) * kBlk + (s & 3) * 32;
-          umma_bf16(tmem + slot * 128, umma_desc_k_sw128(qa + i * kTB + o), umma_desc_k_sw128(ka + st * kTB + o), idesc_s,
-                    s > 0);
+          const int o = ((s >> 2) * kBlk + (s & 3) * 32) / 16;
+          umma_bf16(tmem + slot * 128, a + o, k + o, idesc_s, s > 0);
         }
         umma_commit(&sfull[slot]);
-        if (last_reader) umma_commit(&kempty[st]);
+        if (i == NT - 1) {
+          umma_commit(&kempty[ks_st]);
+          if (++ks_st == p.ring) {
+            ks_st = 0;
+            ks_ph ^= 1;
+          }
+        }
         return true;
       };
-      auto weigh = [&](int i, uint32_t xx, bool first, bool last_reader) {  // O += P V
-        const uint32_t st = xx % p.ring;
+      auto weigh = [&](int i, uint32_t xx, bool first) {  // O += P V
         const uint32_t slot = NT == 1 ? (xx & 1) : i;
-        if (!mbar_wait(&pready[slot], (NT == 1 ? xx >> 1 : xx) & 1, &abort_flag)) return false;
-        if (!mbar_wait(&vfull[st], (xx / p.ring) & 1, &abort_flag)) return false;
+        if (i == 0 && !mbar_wait_short(&vfull[vs_st], vs_ph, &abort_flag)) return false;
+        if (!mbar_wait_short(&pready[slot], (NT == 1 ? xx >> 1 : xx) & 1, &abort_flag)) return false;
         tc_fence_after();
+        const uint64_t v = vd + (uint64_t)(vs_st * (kTB / 16));
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          umma_bf16_ts(tmem + 256 + i * 128, tmem + slot * 128 + s * 8, umma_desc_mn_sw128(va + st * kTB + s * 2048, kBlk),
-                       idesc_o, !first || s > 0);
+          umma_bf16_ts(tmem + 256 + i * 128, tmem + slot * 128 + s * 8, v + s * (2048 / 16), idesc_o, !first || s > 0);
         umma_commit(&pvdone[i]);
-        if (last_reader) umma_commit(&vempty[st]);
+        if (i == NT - 1) {
+          umma_commit(&vempty[vs_st]);
+          if (++vs_st == p.ring) {
+            vs_st = 0;
+            vs_ph ^= 1;
+          }
+        }
         return true;
       };
       for (int j = 0; ok; ++j) {
         const int hb = j & 1;
-        if (!mbar_wait(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
+        if (!mbar_wait_short(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
         if (hdr[hb][kHb] < 0) break;
         const int T = hdr[hb][kHhi] - hdr[hb][kHlo];
         mbar_arrive(&hempty[hb]);
-        if (!mbar_wait(&qfull, j & 1, &abort_flag)) break;
+        if (!mbar_wait_short(&qfull, j & 1, &abort_flag)) break;
         tc_fence_after();
-        for (int i = 0; i < NT && ok; ++i) ok = scores(i, x, i == NT - 1);
+        for (int i = 0; i < NT && ok; ++i) ok = scores(i, x);
         for (int t = 0; t < T && ok; ++t, ++x) {
-          if (NT == 1 && t + 1 < T) ok = scores(0, x + 1, true);
-          if (t + 1 == T) umma_commit(&qempty);  // every product with these queries is issued (NT 1), or is below
+          if (NT == 1 && t + 1 < T) ok = scores(0, x + 1);
+          if (t + 1 == T) umma_commit(&qempty);  // every product with these queries is issued
           for (int i = 0; i < NT && ok; ++i) {
-            if (t == 0 && j > 0) ok = mbar_wait(&ofree[i], (j - 1) & 1, &abort_flag);
-            if (ok) ok = weigh(i, x, t == 0, i == NT - 1);
-            if (NT == 2 && ok && t + 1 < T) ok = scores(i, x + 1, i == 1);
+            if (t == 0 && j > 0) ok = mbar_wait_short(&ofree[i], (j - 1) & 1, &abort_flag);
+            if (ok) ok = weigh(i, x, t == 0);
+            if (NT == 2 && ok && t + 1 < T) ok = scores(i, x + 1);
           }
         }
       }
@@ -641,17 +747,24 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const int r = (warp & 3) * 32 + lane;
     const uint32_t o_addr = tmem + 256 + i * 128 + lane_base;
+    // rows behind a query's last block in use belong to no item: zeros
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+      const int t1 = blocks_of<NT>(p, small ? q_n[b] : drafts_of(p, b)) * NT * p.TT;
+      if (t1 < p.M) {
+        uint4* z = reinterpret_cast<uint4*>(p.out + ((size_t)b * p.M + t1) * p.n_q * D);
+        for (int e = tid; e < (p.M - t1) * p.n_q * (D / 8); e += 128 * NT) z[e] = make_uint4(0, 0, 0, 0);
+      }
+    }
     uint32_t x = 0;
     bool ok = true;
     for (int j = 0; ok; ++j) {
       const int hb = j & 1;
-      if (!warp_wait(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
+      if (!warp_wait_short(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
       const int* h = hdr[hb];
       const int b = h[kHb];
       if (b < 0) break;
-      const int hk = h[kHhk], L = h[kHL], n = h[kHn], Ng = h[kHNg], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
+      const int hk = h[kHhk], sel = h[kHsel], L = h[kHL], n = h[kHn], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
                 hi = h[kHhi], part = h[kHslot];
-      const int* tp = tab + h[kHtab] * 2 * (p.k + 1);
       const int rt = r / p.G, g = r - rt * p.G;
       const int t_row = h[kHt0] + i * p.TT + rt;
       const bool in_use = rt < p.TT && t_row < n;
@@ -660,61 +773,29 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
       for (int t = lo; t < hi; ++t, ++x) {
         // ---- the keys of the tile that this row sees ----
         uint32_t see[4];
-        if (t < Tc) {
-          uint32_t bits = 0;
-          const int gi = t * 16 + lane;
-          if (lane < 16 && gi < Ng) {
-            int a = 0, z = p.k - 1;
-            while (a < z) {
-              const int mid = (a + z + 1) >> 1;
-              if ((tp[mid] >> 3) <= gi) a = mid; else z = mid - 1;
-            }
-            const int g1 = tp[a + 1] >> 3, rest = tp[a] & 7;
-            bits = (gi == g1 - 1 && rest ? (1u << rest) - 1 : 0xFFu) << (8 * (lane & 3));
-          }
-          bits |= __shfl_xor_sync(0xffffffffu, bits, 1);
-          bits |= __shfl_xor_sync(0xffffffffu, bits, 2);
+        const bool drafts = t >= Tc + Tl;
+        const int left = t < Tc ? sel - t * kTile : drafts ? n - (t - Tc - Tl) * kTile : L - (t - Tc) * kTile;
+        const int w0 = (t - Tc - Tl) * (kTile / 32);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) see[q] = __shfl_sync(0xffffffffu, bits, 4 * q);
-        } else {
-          const bool loc = t < Tc + Tl;
-          const int d0 = loc ? (t - Tc) * kTile : (t - Tc - Tl) * kTile;
-          const int left = (loc ? L : n) - d0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int c = left - 32 * q;
-            see[q] = c >= 32 ? ~0u : c > 0 ? (1u << c) - 1 : 0u;
-            if (!loc) see[q] &= in_use && d0 / 32 + q < p.W ? (uint32_t)mk[d0 / 32 + q] : 0u;
-          }
+        for (int q = 0; q < 4; ++q) {
+          const int c = left - 32 * q;
+          see[q] = c >= 32 ? ~0u : c > 0 ? (1u << c) - 1 : 0u;
+          if (drafts) see[q] &= in_use && w0 + q < p.W ? (uint32_t)mk[w0 + q] : 0u;
         }
         const bool all = __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == ~0u);
         const uint32_t slot = NT == 1 ? (x & 1) : i;
         const uint32_t s_addr = tmem + slot * 128 + lane_base;
-        if (!warp_wait(&sfull[slot], (NT == 1 ? x >> 1 : x) & 1, &abort_flag)) {
+        if (!warp_wait_short(&sfull[slot], (NT == 1 ? x >> 1 : x) & 1, &abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // the scores in quarters of 32 keys, twice: for the maximum, then for the weights, which take
-        // the columns of quarters already read
-        float sa[32], sb[32];
-        float m_new;
-        tmem_ld32(s_addr, sa);
-        tmem_ld32(s_addr + 32, sb);
-        tmem_ld_wait_for(sa);
-        tmem_ld_wait_for(sb);
-        m_new = fmaxf(hide_and_max(sa, see[0], all), hide_and_max(sb, see[1], all));
-        tmem_ld32(s_addr + 64, sa);
-        tmem_ld32(s_addr + 96, sb);
-        tmem_ld_wait_for(sa);
-        tmem_ld_wait_for(sb);
-        m_new = fmaxf(m_new, fmaxf(hide_and_max(sa, see[2], all), hide_and_max(sb, see[3], all))) * p.scale_log2;
-        tmem_ld32(s_addr, sa);  // in flight while the reference is settled
+        const float m_new = (all ? row_max<false>(s_addr, see) : row_max<true>(s_addr, see)) * p.scale_log2;
         const bool grow = m_new > m_ref + kSlack || (t == lo && m_new > m_ref);
         const bool need = grow && l > 0.f;
         const bool any = __any_sync(0xffffffffu, need);
         if (any) {  // O holds products with weights of the old reference: rescale
-          if (!warp_wait(&pvdone[i], (x - 1) & 1, &abort_flag)) {
+          if (!warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) {
             ok = false;
             break;
           }
@@ -734,18 +815,11 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
         }
         if (grow) m_ref = m_new;
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float(&cur)[32] = q & 1 ? sb : sa;
-          tmem_ld_wait_for(cur);
-          if (q < 3) tmem_ld32(s_addr + 32 * (q + 1), q & 1 ? sa : sb);
-          if (!all) hide_and_max(cur, see[q], false);
-          l += weigh_quarter(cur, p.scale_log2, neg, s_addr + 16 * q);
-        }
+        l += all ? row_weights<false>(s_addr, see, p.scale_log2, neg) : row_weights<true>(s_addr, see, p.scale_log2, neg);
         tmem_st_wait();
         // the products of the tile before have ended when those of this one may start: one phase of
         // pvdone is outstanding at a time
-        if (t > lo && !any && !warp_wait(&pvdone[i], (x - 1) & 1, &abort_flag)) {
+        if (t > lo && !any && !warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) {
           ok = false;
           break;
         }
@@ -756,13 +830,13 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&hempty[hb]);
-      if (!warp_wait(&pvdone[i], (x - 1) & 1, &abort_flag)) break;
+      if (!warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) break;
       tc_fence_after();
       const bool some = in_use && l != 0.f;  // a NaN sum is kept
       const bool row_out = rt < p.TT && t_row < p.M;
       const float inv = 1.f / l;
       __nv_bfloat16* out = p.out + (((size_t)b * p.M + t_row) * p.n_q + (size_t)hk * p.G + g) * D;
-      float* po = p.part_o + ((size_t)max(part, 0) * (NT * 128) + i * 128 + r) * D;
+      float* po = p.part_o + ((size_t)max(part, 0) * (D / 4) * (NT * 128) + i * 128 + r) * 4;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
@@ -782,7 +856,7 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
         } else {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4*>(po + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            *reinterpret_cast<float4*>(po + (size_t)(c + e) * (NT * 128)) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
         }
       }
       if (part >= 0)
@@ -798,68 +872,61 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
   if (warp == kSoftWarps + 1) tmem_dealloc(tmem, kTmemCols);
 }
 
-// The rows that tree_attend_kernel did not write itself: shared items' parts merged in CTA order,
-// zeros where a query has no drafts in use or no keys.  A warp per (query, draft, head).
+// The items that several CTAs of tree_attend_kernel shared: their parts merged in CTA order.  A CTA
+// takes 1024 / D rows of the item noted by one CTA, a thread 4 elements of a row, neighbouring
+// threads neighbouring rows (as the parts lie); the parts are read once, kAhead of them in flight,
+// with a running maximum.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeP p, int grid) {
-  constexpr int E = D / 32;
+__global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeP p) {
+  constexpr int kRows = 1024 / D, kAhead = 8;
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.B * p.M * p.n_q) return;
-  const int head = (int)(row % p.n_q), t = (int)(row / p.n_q % p.M), b = (int)(row / p.n_q / p.M);
-  const int hk = head / p.G, g = head - hk * p.G;
-  const int n = drafts_of(p, b);
-  const long long base = p.prefix[b], cost = p.prefix[b + 1] - base, W = p.prefix[p.B];
-  const long long n_ctas = min((long long)grid, W);
-  const int rb = t / (NT * p.TT), blocks = blocks_of<NT>(p, n);
-  float acc[E];
+  const int4 it = p.merges[2 * blockIdx.y], cs = p.merges[2 * blockIdx.y + 1];
+  const int b = it.x, n = it.w, c0 = cs.x, c1 = cs.y;
+  if (b < 0) return;
+  const int r = blockIdx.x * kRows + (threadIdx.x & (kRows - 1)), e4 = threadIdx.x / kRows;  // row of the block, elements 4 e4 ..
+  const int i = r >> 7, rt = (r & 127) / p.G, g = (r & 127) - rt * p.G;
+  const int t = it.y + i * p.TT + rt;
+  if (rt >= p.TT || t >= p.M) return;
+  float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  if (t < n) {
+    for (int c = c0; c <= c1; c += kAhead) {
+      float2 ml[kAhead];
+      float4 o[kAhead];
 #pragma unroll
-  for (int e = 0; e < E; ++e) acc[e] = 0.f;
-  float l = 0.f;
-  if (rb < blocks && cost > 0) {
-    const long long T = cost / ((long long)p.n_kv * blocks);
-    const long long w0 = base + ((long long)rb * p.n_kv + hk) * T, w1 = w0 + T - 1;  // the item's tiles
-    // CTA c begins at floor(c W / N): tile w is in the CTA floor(((w + 1) N - 1) / W)
-    const int c0 = (int)(((w0 + 1) * n_ctas - 1) / W), c1 = (int)(((w1 + 1) * n_ctas - 1) / W);
-    if (c0 == c1) return;  // written
-    if (t < n) {
-      const int tr = t - rb * NT * p.TT, i = tr / p.TT;
-      const int r = i * 128 + (tr - i * p.TT) * p.G + g;
-      auto part = [&](int c) -> size_t {
-        const bool first = c > c0 || W * c / n_ctas == w0;
-        return (size_t)(2 * c + (first ? 0 : 1)) * (NT * 128) + r;
-      };
-      float m = -INFINITY;
-      for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[part(c) * 2]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float mu = m == -INFINITY ? 0.f : m;
-#pragma unroll 4
-      for (int c = c0; c <= c1; ++c) {
-        const size_t pr = part(c);
-        const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + pr * 2);
-        // an empty part (no key seen) has weight 0 whatever its row of O holds
-        const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - mu);
-        l = fmaf(f, ml.y, l);
-        float v[E];
-        if constexpr (E == 4) {
-          const float4 x4 = *reinterpret_cast<const float4*>(p.part_o + pr * D + lane * 4);
-          v[0] = x4.x; v[1] = x4.y; v[2] = x4.z; v[3] = x4.w;
-        } else {
-          const float2 x2 = *reinterpret_cast<const float2*>(p.part_o + pr * D + lane * 2);
-          v[0] = x2.x; v[1] = x2.y;
+      for (int u = 0; u < kAhead; ++u) {
+        ml[u] = make_float2(-INFINITY, 0.f);
+        if (c + u <= c1) {
+          const size_t slot = c + u > c0 ? 2 * (size_t)(c + u) : (size_t)cs.z;
+          ml[u] = *reinterpret_cast<const float2*>(p.part_ml + (slot * (NT * 128) + r) * 2);
+          o[u] = *reinterpret_cast<const float4*>(p.part_o + ((slot * (D / 4) + e4) * (NT * 128) + r) * 4);
         }
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
       }
+      float mx = m;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) mx = fmaxf(mx, ml[u].x);
+      const float mu = mx == -INFINITY ? 0.f : mx;
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mu);
+      l *= f0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] *= f0;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (c + u > c1) break;
+        // a part that saw no key has reference -inf (and zeros in O); a NaN reference stays NaN
+        const float f = ml[u].x == -INFINITY ? 0.f : ex2(ml[u].x - mu);
+        l = fmaf(f, ml[u].y, l);
+        acc[0] = fmaf(f, o[u].x, acc[0]);
+        acc[1] = fmaf(f, o[u].y, acc[1]);
+        acc[2] = fmaf(f, o[u].z, acc[2]);
+        acc[3] = fmaf(f, o[u].w, acc[3]);
+      }
+      m = mx;
     }
   }
   const float inv = 1.f / l;
-#pragma unroll
-  for (int e = 0; e < E; e += 2)
-    *reinterpret_cast<uint32_t*>(p.out + row * D + lane * E + e) =
-        l > 0.f || l != l ? pack_bf16x2(acc[e] * inv, acc[e + 1] * inv) : 0u;
+  uint2 v = make_uint2(0, 0);
+  if (l != 0.f) v = make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+  *reinterpret_cast<uint2*>(p.out + (((size_t)b * p.M + t) * p.n_q + (size_t)it.z * p.G + g) * D + 4 * e4) = v;
 }
 
 // drafts per row tile, row tiles per CTA, row blocks per query
@@ -877,8 +944,8 @@ TreeShape tree_shape(const msa_dims& d, int M) {
 template <int D, int NT>
 cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   const int tile = D / 64 * kTile * 128;
-  const size_t tables = (size_t)4 * (p.k + 1) * sizeof(int);
-  constexpr size_t kDyn = 227 * 1024 - 832;  // less the statically sized part
+  const size_t tables = (size_t)2 * (p.k + 1) * sizeof(int);
+  constexpr size_t kDyn = 227 * 1024 - 1344;  // less the statically sized part
   p.ring = (int)std::min<size_t>(kMaxRing, (kDyn - 1024 - tables - NT * tile) / (2 * tile));
   const size_t smem = 1024 + (size_t)(NT + 2 * p.ring) * tile + tables;
   auto kern = tree_attend_kernel<D, NT>;
@@ -891,21 +958,22 @@ cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   TraceScope ts(kKTreeCombine, s);
-  const int64_t rows = (int64_t)p.B * p.M * p.n_q;
-  return launch_pdl(tree_combine_kernel<D, NT>, dim3((unsigned)((rows + 7) / 8)), dim3(256), 0, s, p, n_ctas);
+  constexpr int kRows = 1024 / D;
+  const int row_groups = NT == 1 ? (p.M * p.G + kRows - 1) / kRows : NT * 128 / kRows;
+  return launch_pdl(tree_combine_kernel<D, NT>, dim3(row_groups, n_ctas), dim3(256), 0, s, p);
 }
 
 struct TreeWs {
-  int64_t* prefix;
-  int32_t* groups;
+  int4* merges;
+  int32_t* sel;
   float *part_ml, *part_o;
 };
 size_t tree_carve(const msa_dims& d, int B, int M, void* ws, TreeWs* out) {
   const TreeShape sh = tree_shape(d, M);
   Carver cv(ws);
   TreeWs w;
-  w.prefix = cv.take<int64_t>((size_t)B + 1);
-  w.groups = cv.take<int32_t>((size_t)B);
+  w.merges = cv.take<int4>((size_t)2 * sm_count());
+  w.sel = cv.take<int32_t>((size_t)B);
   w.part_ml = cv.take<float>((size_t)2 * sm_count() * sh.NT * 128 * 2);
   w.part_o = cv.take<float>((size_t)2 * sm_count() * sh.NT * 128 * d.head_dim);
   if (out) *out = w;
@@ -950,12 +1018,9 @@ msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaSt
   p.loc_len = c.loc_len;
   p.chunk_off = c.chunk_off;
   p.topk_idx = c.topk_idx;
-  p.V_draft = static_cast<const __nv_bfloat16*>(c.V_draft);
-  p.V_loc = static_cast<const __nv_bfloat16*>(c.V_loc);
-  p.V_bar = static_cast<const __nv_bfloat16*>(c.V_bar);
   p.out = static_cast<__nv_bfloat16*>(c.out);
-  p.prefix = w.prefix;
-  p.groups = w.groups;
+  p.merges = w.merges;
+  p.sel = w.sel;
   p.part_o = w.part_o;
   p.part_ml = w.part_ml;
   p.B = c.B;
@@ -990,23 +1055,18 @@ msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaSt
                                   CU_TENSOR_MAP_SWIZZLE_128B);
   };
   msa_status st = map4(&maps.q, c.q, d.n_q, c.M, qrow, p.G, p.TT);
-  if (st == MSA_OK) st = map4(&maps.kd8, c.K_draft, d.n_kv, c.M, row, 1, 8);
-  if (st == MSA_OK) st = map4(&maps.vd8, c.V_draft, d.n_kv, c.M, row, 1, 8);
-  if (c.t_loc_max > 0) {
-    if (st == MSA_OK) st = map4(&maps.kl128, c.K_loc, d.n_kv, c.t_loc_max, row, 1, kTile);
-    if (st == MSA_OK) st = map4(&maps.vl128, c.V_loc, d.n_kv, c.t_loc_max, row, 1, kTile);
-    if (st == MSA_OK) st = map4(&maps.kl8, c.K_loc, d.n_kv, c.t_loc_max, row, 1, 8);
-    if (st == MSA_OK) st = map4(&maps.vl8, c.V_loc, d.n_kv, c.t_loc_max, row, 1, 8);
-  }
-  if (c.k > 0) {
-    if (st == MSA_OK) st = map3(&maps.kb8, c.K_bar, 8);
-    if (st == MSA_OK) st = map3(&maps.vb8, c.V_bar, 8);
+  const void* src[3][2] = {{c.K_bar, c.V_bar}, {c.K_loc, c.V_loc}, {c.K_draft, c.V_draft}};
+  for (int kv = 0; kv < 2; ++kv) {
+    for (int i = 0; i < 3 && c.k > 0 && st == MSA_OK; ++i) st = map3(&maps.bar[kv][i], src[0][kv], kBoxRows[i]);
+    for (int i = 0; i < 4 && c.t_loc_max > 0 && st == MSA_OK; ++i)
+      st = map4(&maps.loc[kv][i], src[1][kv], d.n_kv, c.t_loc_max, row, 1, kBoxRows[i]);
+    for (int i = 0; i < 2 && st == MSA_OK; ++i) st = map4(&maps.draft[kv][i], src[2][kv], d.n_kv, c.M, row, 1, kBoxRows[i]);
   }
   if (st != MSA_OK) return st;
   if (c.k > 0 && c.B > kSmallB) {
     TraceScope ts(kKTreePlan, s);
-    MSA_CUDA_CHECK(launch_pdl(tree_groups_kernel, dim3((c.B + 7) / 8), dim3(256), 0, s, c.topk_idx, c.chunk_off, c.B,
-                              c.k, c.n_docs, c.n_chunks, w.groups));
+    MSA_CUDA_CHECK(launch_pdl(tree_select_kernel, dim3((c.B + 7) / 8), dim3(256), 0, s, c.topk_idx, c.chunk_off, c.B,
+                              c.k, c.n_docs, c.n_chunks, w.sel));
   }
   cudaError_t e = d.head_dim == 128 ? (sh.NT == 2 ? launch_attend<128, 2>(maps, p, s) : launch_attend<128, 1>(maps, p, s))
                                     : (sh.NT == 2 ? launch_attend<64, 2>(maps, p, s) : launch_attend<64, 1>(maps, p, s));
