@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 __all__ = [
@@ -82,11 +83,8 @@ class Rotary(ctypes.Structure):
                 ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
-class _Heads(ctypes.Structure):
-    """msa_heads: strided heads of a call's rows, read (inp) and written (out)."""
-    _fields_ = [("inp", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_row", ctypes.c_int64),
-                ("in_head", ctypes.c_int64), ("out_row", ctypes.c_int64), ("out_head", ctypes.c_int64),
-                ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+# msa_heads: in, out, in_row, in_head, out_row, out_head, heads, reserved
+_HEADS = struct.Struct("@PPqqqqii")
 
 
 def _load():
@@ -96,7 +94,8 @@ def _load():
             "(nvcc, sm_100a). There is no CPU fallback.")
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    DP, RP, HP = ctypes.POINTER(Dims), ctypes.POINTER(Rotary), ctypes.POINTER(_Heads)
+    DP = ctypes.POINTER(Dims)
+    RP = HP = P  # msa_rotary by address, msa_heads as packed bytes (_heads)
     sig = {
         "msa_last_error": (ctypes.c_char_p, []),
         "msa_version": (I32, []),
@@ -134,8 +133,8 @@ def _load():
         "msa_head_norm_rotate_grad": (I32, [RP, I32, HP, HP, HP, HP, I64, P, P, F, F, P, P, P, P, SZ, P]),
         "msa_tree_plan": (I32, [P, P, P, I32, I32, I32, P, P, P]),
         "msa_tree_attend_workspace_size": (SZ, [DP, I32, I32, I32, I32]),
-        "msa_tree_attend": (I32, [DP, P, P, P, P, P, I32, I32, P, P, P, I32, P, P, P, I32, I32, P, I32, F, P, P, SZ, P]),
-        "msa_tree_commit": (I32, [DP, P, P, P, P, I32, I32, I32, P, P, P, I32, P, P]),
+        "msa_tree_attend": (I32, [P, P, P, P, P, P, I32, I32, P, P, P, I32, P, P, P, I32, I32, P, I32, F, P, P, SZ, P]),
+        "msa_tree_commit": (I32, [P, P, P, P, P, I32, I32, I32, P, P, P, I32, P, P]),
         "msa_trace_enable": (I32, [I32]),
         "msa_trace_reset": (I32, []),
         "msa_trace_num_kernels": (I32, []),
@@ -158,7 +157,9 @@ class _LazyLib:
     def __getattr__(self, name):
         if _LazyLib._cdll is None:
             _LazyLib._cdll = _load()
-        return getattr(_LazyLib._cdll, name)
+        fn = getattr(_LazyLib._cdll, name)
+        self.__dict__[name] = fn  # the next use finds it at once
+        return fn
 
 
 lib = _LazyLib()
@@ -548,7 +549,7 @@ def attend_merge(o_shares, lse2_shares, out=None, stream=None):
 # ----------------------------------------------------------------------------
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
-_DTYPES: dict = {}  # torch dtype -> msa_dtype (filled on first use: the module imports without torch)
+_DTYPES: dict = {}  # torch dtype -> msa_dtype (filled on first use)
 
 
 def rotary(head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", base: float = 1e6,
@@ -574,98 +575,99 @@ def rotary_turns(rot: Rotary):
     import numpy as np
 
     out = np.zeros(max(1, rot.rot_dim // 2), dtype=np.uint64)
-    _check(lib.msa_rotary_turns(ctypes.byref(rot), out.ctypes.data))
+    _check(lib.msa_rotary_turns(ctypes.addressof(rot), out.ctypes.data))
     return out
 
 
-def _dtype_code(dtype, name: str) -> int:
-    if not _DTYPES:
-        import torch
+def _bind_torch() -> None:
+    """Fill the module's torch names (the module imports without torch)."""
+    global _torch, _cur_device, _raw_stream
+    import torch
 
-        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    _cur_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _torch = torch
+
+
+_torch = None
+_cur_device = _raw_stream = None
+
+
+def _on_device(t, name: str) -> int:
+    """The index of t's CUDA device, which must be the current one (the library launches there)."""
+    if _torch is None:
+        _bind_torch()
+    dev = t.get_device()
+    if dev < 0 or not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor, got {t.device}")
+    if dev != _cur_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_cur_device()}")
+    return dev
+
+
+def _dtype_code(dtype, name: str) -> int:
     code = _DTYPES.get(dtype)
     if code is None:
         raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, got {dtype}")
     return code
 
 
-def _on_device(t, name: str):
-    """The CUDA device of t, which must be the current one (the library launches there)."""
-    import torch
-
-    dev = t.device
-    if dev.type != "cuda":
-        raise ValueError(f"{name}: expected a CUDA tensor, got {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {dev}, but the current device is cuda:{torch.cuda.current_device()}")
-    return dev
+def _flat(t, name: str, shape, dtype, dev: int) -> int:
+    """The address of t, which must be a contiguous tensor of this shape and dtype on device dev."""
+    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
 
 
-def _head_shape(t, name: str, rot: Rotary, rows, heads, dtype, device) -> None:
-    """Raise ValueError unless t is [rows, heads, head_dim] with contiguous head elements (rows or
-    heads None: any)."""
-    sh = t.shape
-    if (len(sh) != 3 or sh[2] != rot.head_dim or (rows is not None and sh[0] != rows)
-            or (heads is not None and sh[1] != heads) or sh[1] < 1):
-        raise ValueError(f"{name}: expected [{'rows' if rows is None else rows}, {'heads' if heads is None else heads}, "
-                         f"{rot.head_dim}], got {tuple(sh)}")
-    if t.dtype != dtype or t.device != device or t.stride(2) != 1:
-        raise ValueError(f"{name}: expected {dtype} on {device} with contiguous head elements, got {t.dtype} on "
-                         f"{t.device}, strides {t.stride()}")
-
-
-def _heads(t, out=None) -> _Heads:
-    st = t.stride()
+def _heads(x, out, name: str, rows: int, head_dim: int, dtype, dev: int) -> bytes:
+    """msa_heads of x [rows, heads, head_dim], its output in ``out`` (None: no output) of the same
+    shape; both with any strides but contiguous head elements."""
+    sx = x.stride()
+    if x.dim() != 3 or x.dtype != dtype or x.get_device() != dev or sx[2] != 1:
+        raise ValueError(f"{name}: expected [rows, heads, {head_dim}] {dtype} on cuda:{dev} with contiguous head "
+                         f"elements, got {tuple(x.shape)} {x.dtype} on {x.device}, strides {sx}")
+    sh = x.shape
+    if sh[0] != rows or sh[2] != head_dim or sh[1] < 1:
+        raise ValueError(f"{name}: expected [{rows}, heads, {head_dim}], got {tuple(sh)}")
     if out is None:
-        return _Heads(t.data_ptr(), None, st[0], st[1], 0, 0, t.shape[1], 0)
+        return _HEADS.pack(x.data_ptr(), 0, sx[0], sx[1], 0, 0, sh[1], 0)
     so = out.stride()
-    return _Heads(t.data_ptr(), out.data_ptr(), st[0], st[1], so[0], so[1], t.shape[1], 0)
+    if out.shape != sh or out.dtype != dtype or out.get_device() != dev or so[2] != 1:
+        raise ValueError(f"the output of {name}: expected {tuple(sh)} {dtype} on cuda:{dev} with contiguous head "
+                         f"elements, got {tuple(out.shape)} {out.dtype} on {out.device}, strides {so}")
+    return _HEADS.pack(x.data_ptr(), out.data_ptr(), sx[0], sx[1], so[0], so[1], sh[1], 0)
+
+
+def _launch_stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream(stream)
 
 
 def _used_on(stream, *tensors) -> None:
     """Tell the allocator that tensors allocated here are used on the caller's ``stream``."""
-    if stream is None:
+    if stream is None or not tensors:
         return
-    import torch
-
-    st = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    if st != torch.cuda.current_stream():
+    st = _torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+    if st != _torch.cuda.current_stream():
         for t in tensors:
             if t is not None:
                 t.record_stream(st)
 
 
-def _norm_weights(rot, q_weight, k_weight, dtype, device) -> None:
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _expect(w, name, (rot.head_dim,), dtype, device)
+def _norm_weight(w, name: str, rot: Rotary, dtype, dev: int):
+    return None if w is None else _flat(w, name, (rot.head_dim,), dtype, dev)
 
 
-def _rot_args(rot, q, k, positions, out, k_out):
-    """Checks shared by the rotation and norm calls; allocates missing outputs."""
-    import torch
-
+def _rows_of(rot, q, positions):
+    """(device, dtype, rows, address of the positions) of a call on heads q."""
     dev = _on_device(q, "q")
-    code = _dtype_code(q.dtype, "q")
-    _head_shape(q, "q", rot, None, None, q.dtype, dev)
-    rows = q.shape[0]
-    _expect(positions, "positions", (rows,), torch.int32, dev)
-    new = []
-    if out is None:
-        out = torch.empty(tuple(q.shape), dtype=q.dtype, device=dev)
-        new.append(out)
-    else:
-        _head_shape(out, "out", rot, rows, q.shape[1], q.dtype, dev)
-    if k is not None:
-        _head_shape(k, "k", rot, rows, None, q.dtype, dev)
-        if k_out is None:
-            k_out = torch.empty(tuple(k.shape), dtype=q.dtype, device=dev)
-            new.append(k_out)
-        else:
-            _head_shape(k_out, "k_out", rot, rows, k.shape[1], q.dtype, dev)
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    return code, rows, out, k_out, new
+    rows = q.shape[0] if q.dim() == 3 else -1
+    if rows < 0:
+        raise ValueError(f"q: expected [rows, heads, {rot.head_dim}], got {tuple(q.shape)}")
+    return dev, q.dtype, rows, _flat(positions, "positions", (rows,), _torch.int32, dev)
 
 
 def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_out=None, stream=None):
@@ -674,9 +676,23 @@ def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_ou
     bf16, fp16 or fp32; rows and heads may be strided (slices of a fused projection).  ``out`` /
     ``k_out`` may be q / k themselves (in place).  ``grad`` applies the transposed rotation: the
     gradient of the call, given the gradient of its output.  Returns out, or (out, k_out) with k."""
-    code, rows, out, k_out, new = _rot_args(rot, q, k, positions, out, k_out)
-    _check(lib.msa_rotate(ctypes.byref(rot), code, _heads(q, out), None if k is None else _heads(k, k_out), rows,
-                          positions.data_ptr(), 1 if grad else 0, _stream(stream)))
+    dev, dt, rows, pos = _rows_of(rot, q, positions)
+    code, D = _dtype_code(dt, "q"), rot.head_dim
+    new = ()
+    if out is None:
+        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        new = (out,)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        hk = None
+    else:
+        if k_out is None:
+            k_out = _torch.empty_like(k, memory_format=_torch.contiguous_format)
+            new += (k_out,)
+        hk = _heads(k, k_out, "k", rows, D, dt, dev)
+    _check(lib.msa_rotate(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, rows, pos,
+                          1 if grad else 0, _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
@@ -686,11 +702,24 @@ def head_norm_rotate(rot: Rotary, q, k, q_weight, k_weight, positions, eps: floa
     """RMS norm of every query and key head, times (weight_offset + weight), then the rotation, in
     one pass.  q, k [rows, heads, head_dim] as for ``rotate`` (k may be None); weights [head_dim] of
     the same dtype, or None.  Returns (out, k_out), or out without k."""
-    code, rows, out, k_out, new = _rot_args(rot, q, k, positions, out, k_out)
-    _norm_weights(rot, q_weight, k_weight, q.dtype, q.device)
-    _check(lib.msa_head_norm_rotate(ctypes.byref(rot), code, _heads(q, out), None if k is None else _heads(k, k_out),
-                                    rows, _ptr(q_weight), _ptr(k_weight), weight_offset, eps, positions.data_ptr(),
-                                    _stream(stream)))
+    dev, dt, rows, pos = _rows_of(rot, q, positions)
+    code, D = _dtype_code(dt, "q"), rot.head_dim
+    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
+    new = ()
+    if out is None:
+        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        new = (out,)
+    if k is None:
+        if k_out is not None:
+            raise ValueError("k_out without k")
+        hk = None
+    else:
+        if k_out is None:
+            k_out = _torch.empty_like(k, memory_format=_torch.contiguous_format)
+            new += (k_out,)
+        hk = _heads(k, k_out, "k", rows, D, dt, dev)
+    _check(lib.msa_head_norm_rotate(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, rows, wq, wk,
+                                    weight_offset, eps, pos, _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
@@ -701,28 +730,29 @@ def head_norm_append(rot: Rotary, q, k, v, q_weight, k_weight, positions, slots,
     (normalised, rotated) and the values to row ``slots[r]`` of their query's local cache
     K_loc, V_loc [B, t_loc_max, n_kv, head_dim] (rows / B rows per query, in order).  A slot of -1
     leaves the row out of the cache.  Returns out."""
-    import torch
-
-    code, rows, out, _, new = _rot_args(rot, q, None, positions, out, None)
-    dt, dev = q.dtype, q.device
-    _head_shape(k, "k", rot, rows, None, dt, dev)
-    _head_shape(v, "v", rot, rows, k.shape[1], dt, dev)
-    _norm_weights(rot, q_weight, k_weight, dt, dev)
-    _expect(slots, "slots", (rows,), torch.int32, dev)
-    if K_loc.dim() != 4:
-        raise ValueError(f"K_loc: expected [B, t_loc_max, n_kv, head_dim], got {tuple(K_loc.shape)}")
+    dev, dt, rows, pos = _rows_of(rot, q, positions)
+    code, D = _dtype_code(dt, "q"), rot.head_dim
+    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
+    new = ()
+    if out is None:
+        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        new = (out,)
+    hk, hv = _heads(k, None, "k", rows, D, dt, dev), _heads(v, None, "v", rows, D, dt, dev)
+    if K_loc.dim() != 4 or v.shape != k.shape:
+        raise ValueError(f"expected K_loc [B, t_loc_max, n_kv, head_dim] and v of k's shape, got {tuple(K_loc.shape)}, "
+                         f"{tuple(v.shape)}, {tuple(k.shape)}")
     B, t_loc_max = K_loc.shape[0], K_loc.shape[1]
-    for name, t in (("K_loc", K_loc), ("V_loc", V_loc)):
-        _expect(t, name, (B, t_loc_max, k.shape[1], rot.head_dim), dt, dev)
-    _check(lib.msa_head_norm_append(ctypes.byref(rot), code, _heads(q, out), _heads(k), _heads(v), rows, _ptr(q_weight),
-                                    _ptr(k_weight), weight_offset, eps, positions.data_ptr(), slots.data_ptr(),
-                                    K_loc.data_ptr(), V_loc.data_ptr(), B, t_loc_max, _stream(stream)))
+    cache = (B, t_loc_max, k.shape[1], D)
+    _check(lib.msa_head_norm_append(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, hv, rows, wq,
+                                    wk, weight_offset, eps, pos, _flat(slots, "slots", (rows,), _torch.int32, dev),
+                                    _flat(K_loc, "K_loc", cache, dt, dev), _flat(V_loc, "V_loc", cache, dt, dev), B,
+                                    t_loc_max, _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out
 
 
 def head_norm_grad_workspace_size(rot: Rotary, rows: int, n_q: int, n_k: int) -> int:
-    return int(lib.msa_head_norm_grad_workspace_size(ctypes.byref(rot), rows, n_q, n_k))
+    return int(lib.msa_head_norm_grad_workspace_size(ctypes.addressof(rot), rows, n_q, n_k))
 
 
 def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, dk, eps: float = 1e-6,
@@ -731,37 +761,38 @@ def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, 
 
     Returns (gradient of q, of k, of q_weight [head_dim] fp32, of k_weight fp32); ``out`` takes the
     four tensors.  k and dk may be None together (the second and fourth are then None)."""
-    import torch
-
     if (k is None) != (dk is None):
         raise ValueError("k and dk go together")
-    o = (None,) * 4 if out is None else out
-    code, rows, gq, gk, new = _rot_args(rot, q, k, positions, o[0], o[1])
-    dt, dev = q.dtype, q.device
-    _head_shape(dq, "dq", rot, rows, q.shape[1], dt, dev)
-    if dk is not None:
-        _head_shape(dk, "dk", rot, rows, k.shape[1], dt, dev)
-    _norm_weights(rot, q_weight, k_weight, dt, dev)
-    dw = []
-    for name, t, used in (("out[2]", o[2], True), ("out[3]", o[3], k is not None)):
-        if t is None and used:
-            t = torch.empty(rot.head_dim, dtype=torch.float32, device=dev)
-            new.append(t)
-        elif t is not None:
-            _expect(t, name, (rot.head_dim,), torch.float32, dev)
-        dw.append(t)
-    nbytes = head_norm_grad_workspace_size(rot, rows, q.shape[1], 0 if k is None else k.shape[1])
+    dev, dt, rows, pos = _rows_of(rot, q, positions)
+    code, D = _dtype_code(dt, "q"), rot.head_dim
+    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
+    hq = _heads(q, None, "q", rows, D, dt, dev)
+    hk = None if k is None else _heads(k, None, "k", rows, D, dt, dev)
+    f32, new = _torch.float32, []
+    if out is None:
+        gq = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        gk = None if k is None else _torch.empty_like(k, memory_format=_torch.contiguous_format)
+        gwq = _torch.empty(D, dtype=f32, device=q.device)
+        gwk = None if k is None else _torch.empty(D, dtype=f32, device=q.device)
+        new = [gq, gk, gwq, gwk]
+    else:
+        gq, gk, gwq, gwk = out
+    if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
+        raise ValueError("dq and dk must have the shapes of q and k")
+    hdq = _heads(dq, gq, "dq", rows, D, dt, dev)
+    hdk = None if k is None else _heads(dk, gk, "dk", rows, D, dt, dev)
+    awq = None if gwq is None else _flat(gwq, "out[2]", (D,), f32, dev)
+    awk = None if gwk is None else _flat(gwk, "out[3]", (D,), f32, dev)
     if ws is None:
-        ws = _workspace(nbytes, dev)
+        nbytes = head_norm_grad_workspace_size(rot, rows, q.shape[1], 0 if k is None else k.shape[1])
+        ws = _workspace(nbytes, q.device)
         new.append(ws)
     else:  # the library checks the caller's buffer against what it needs
         nbytes = max(0, ws.numel() * ws.element_size() - 256)
-    _check(lib.msa_head_norm_rotate_grad(
-        ctypes.byref(rot), code, _heads(q), None if k is None else _heads(k), _heads(dq, gq),
-        None if k is None else _heads(dk, gk), rows, _ptr(q_weight), _ptr(k_weight), weight_offset, eps,
-        positions.data_ptr(), _ptr(dw[0]), _ptr(dw[1]), _aligned_ptr(ws), nbytes, _stream(stream)))
+    _check(lib.msa_head_norm_rotate_grad(ctypes.addressof(rot), code, hq, hk, hdq, hdk, rows, wq, wk, weight_offset, eps,
+                                         pos, awq, awk, _aligned_ptr(ws), nbytes, _launch_stream(stream, dev)))
     _used_on(stream, *new)
-    return gq, gk, dw[0], dw[1]
+    return gq, gk, gwq, gwk
 
 
 # ----------------------------------------------------------------------------
@@ -772,25 +803,21 @@ def tree_plan(parents, loc_len, pos_offset: int, n_draft=None, out=None, stream=
 
     ``parents`` [B, M] int32: an earlier draft, or -1 for one that follows the committed context of
     ``loc_len`` [B] tokens; ``n_draft`` [B] int32: drafts in use (None: all)."""
-    import torch
-
     dev = _on_device(parents, "parents")
     if parents.dim() != 2:
         raise ValueError(f"parents: expected [B, M], got {tuple(parents.shape)}")
-    B, M = parents.shape
-    _expect(parents, "parents", (B, M), torch.int32, dev)
-    _expect(loc_len, "loc_len", (B,), torch.int32, dev)
-    if n_draft is not None:
-        _expect(n_draft, "n_draft", (B,), torch.int32, dev)
+    i32 = _torch.int32
+    shape = parents.shape
+    B, M = shape
+    words = (B, M, (M + 31) // 32)
     new = ()
     if out is None:
-        out = new = (torch.empty((B, M, (M + 31) // 32), dtype=torch.int32, device=dev),
-                     torch.empty((B, M), dtype=torch.int32, device=dev))
-    else:
-        _expect(out[0], "out[0]", (B, M, (M + 31) // 32), torch.int32, dev)
-        _expect(out[1], "out[1]", (B, M), torch.int32, dev)
-    _check(lib.msa_tree_plan(parents.data_ptr(), _ptr(n_draft), loc_len.data_ptr(), B, M, pos_offset, out[0].data_ptr(),
-                             out[1].data_ptr(), _stream(stream)))
+        out = new = (_torch.empty(words, dtype=i32, device=parents.device), _torch.empty_like(parents, dtype=i32))
+    _check(lib.msa_tree_plan(_flat(parents, "parents", shape, i32, dev),
+                             None if n_draft is None else _flat(n_draft, "n_draft", (B,), i32, dev),
+                             _flat(loc_len, "loc_len", (B,), i32, dev), B, M, pos_offset,
+                             _flat(out[0], "out[0]", words, i32, dev), _flat(out[1], "out[1]", shape, i32, dev),
+                             _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out
 
@@ -809,58 +836,52 @@ def tree_attend(dims, q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft=
     ``tree_plan``'s positions).  ``mask`` [B, M, ceil(M/32)] int32 from ``tree_plan``.  The memory
     arguments (as for ``sparse_attend``) go together; without them the drafts attend over cache and
     drafts alone.  A draft t >= n_draft[b] and a row that sees no key give zeros."""
-    import torch
-
     dd = Dims.of(dims)
     dev = _on_device(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q: expected [B, M, n_q, head_dim], got {tuple(q.shape)}")
     B, M = q.shape[0], q.shape[1]
-    bf, i32 = torch.bfloat16, torch.int32
-    kv = (dd.n_kv, dd.head_dim)
-    _expect(q, "q", (B, M, dd.n_q, dd.head_dim), bf, dev)
-    _expect(K_draft, "K_draft", (B, M) + kv, bf, dev)
-    _expect(V_draft, "V_draft", (B, M) + kv, bf, dev)
-    _expect(mask, "mask", (B, M, (M + 31) // 32), i32, dev)
-    _expect(loc_len, "loc_len", (B,), i32, dev)
-    if n_draft is not None:
-        _expect(n_draft, "n_draft", (B,), i32, dev)
-    t_loc_max = 0
+    bf, i32 = _torch.bfloat16, _torch.int32
+    n_kv, D = dd.n_kv, dd.head_dim
+    rows = (B, M, dd.n_q, D)
+    drafts = (B, M, n_kv, D)
     if (K_loc is None) != (V_loc is None):
         raise ValueError("K_loc and V_loc go together")
+    t_loc_max, kl, vl = 0, None, None
     if K_loc is not None:
         t_loc_max = K_loc.shape[1] if K_loc.dim() == 4 else -1
-        _expect(K_loc, "K_loc", (B, t_loc_max) + kv, bf, dev)
-        _expect(V_loc, "V_loc", (B, t_loc_max) + kv, bf, dev)
-    memory = (K_bar, V_bar, chunk_off, topk_idx)
+        cache = (B, t_loc_max, n_kv, D)
+        kl, vl = _flat(K_loc, "K_loc", cache, bf, dev), _flat(V_loc, "V_loc", cache, bf, dev)
+        if t_loc_max == 0:
+            kl = vl = None
     k = n_docs = n_chunks = 0
-    if any(x is not None for x in memory):
-        if any(x is None for x in memory):
+    kb = vb = co = top = None
+    if K_bar is not None or V_bar is not None or chunk_off is not None or topk_idx is not None:
+        if K_bar is None or V_bar is None or chunk_off is None or topk_idx is None:
             raise ValueError("K_bar, V_bar, chunk_off and topk_idx go together")
         k, n_docs, n_chunks = topk_idx.shape[-1], chunk_off.numel() - 1, K_bar.shape[0]
-        _expect(K_bar, "K_bar", (n_chunks,) + kv, bf, dev)
-        _expect(V_bar, "V_bar", (n_chunks,) + kv, bf, dev)
-        _expect(chunk_off, "chunk_off", (n_docs + 1,), i32, dev)
-        _expect(topk_idx, "topk_idx", (B, k), i32, dev)
+        memory = (n_chunks, n_kv, D)
+        kb, vb = _flat(K_bar, "K_bar", memory, bf, dev), _flat(V_bar, "V_bar", memory, bf, dev)
+        co, top = _flat(chunk_off, "chunk_off", (n_docs + 1,), i32, dev), _flat(topk_idx, "topk_idx", (B, k), i32, dev)
         if k == 0:
-            K_bar = V_bar = chunk_off = topk_idx = None
+            kb = vb = co = top = None
     new = []
     if out is None:
-        out = torch.empty(tuple(q.shape), dtype=bf, device=dev)
+        out = _torch.empty_like(q)
         new.append(out)
-    else:
-        _expect(out, "out", tuple(q.shape), bf, dev)
     if ws is not None:  # the library checks the caller's buffer against what it needs
         nbytes = max(0, ws.numel() * ws.element_size() - 256)
     else:
         nbytes = tree_attend_workspace_size(dims, B, M, k, t_loc_max)
-        ws = _workspace(nbytes, dev)
+        ws = _workspace(nbytes, q.device)
         new.append(ws)
-    _check(lib.msa_tree_attend(ctypes.byref(dd), q.data_ptr(), K_draft.data_ptr(), V_draft.data_ptr(), mask.data_ptr(),
-                               _ptr(n_draft), B, M, _ptr(K_loc) if t_loc_max else None,
-                               _ptr(V_loc) if t_loc_max else None, loc_len.data_ptr(), t_loc_max, _ptr(K_bar),
-                               _ptr(V_bar), _ptr(chunk_off), n_docs, n_chunks, _ptr(topk_idx), k, float(softmax_scale),
-                               out.data_ptr(), _aligned_ptr(ws), nbytes, _stream(stream)))
+    _check(lib.msa_tree_attend(ctypes.addressof(dd), _flat(q, "q", rows, bf, dev),
+                               _flat(K_draft, "K_draft", drafts, bf, dev), _flat(V_draft, "V_draft", drafts, bf, dev),
+                               _flat(mask, "mask", (B, M, (M + 31) // 32), i32, dev),
+                               None if n_draft is None else _flat(n_draft, "n_draft", (B,), i32, dev), B, M, kl, vl,
+                               _flat(loc_len, "loc_len", (B,), i32, dev), t_loc_max, kb, vb, co, n_docs, n_chunks, top,
+                               k, softmax_scale, _flat(out, "out", rows, bf, dev), _aligned_ptr(ws), nbytes,
+                               _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out
 
@@ -869,29 +890,23 @@ def tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out=None,
     """Append the accepted drafts to the local caches: row path[b, i] of K_draft / V_draft
     [B, M, n_kv, head_dim] to slot loc_len[b] + i of K_loc / V_loc, for i < n_path[b].  Returns the
     new lengths [B] int32 (``out``, which must not be ``loc_len``)."""
-    import torch
-
     dev = _on_device(K_draft, "K_draft")
     if K_draft.dim() != 4 or K_loc.dim() != 4 or path.dim() != 2:
         raise ValueError("expected K_draft [B, M, n_kv, head_dim], K_loc [B, t_loc_max, n_kv, head_dim], path [B, A]")
-    B, M, n_kv, D = K_draft.shape
+    drafts = K_draft.shape
+    B, M, n_kv, D = drafts
     t_loc_max, A = K_loc.shape[1], path.shape[1]
-    bf, i32 = torch.bfloat16, torch.int32
-    for name, t, n in (("K_draft", K_draft, M), ("V_draft", V_draft, M), ("K_loc", K_loc, t_loc_max),
-                       ("V_loc", V_loc, t_loc_max)):
-        _expect(t, name, (B, n, n_kv, D), bf, dev)
-    _expect(path, "path", (B, A), i32, dev)
-    _expect(n_path, "n_path", (B,), i32, dev)
-    _expect(loc_len, "loc_len", (B,), i32, dev)
+    cache, one = (B, t_loc_max, n_kv, D), (B,)
+    bf, i32 = _torch.bfloat16, _torch.int32
     new = ()
     if out is None:
-        out = torch.empty(B, dtype=i32, device=dev)
+        out = _torch.empty(B, dtype=i32, device=K_draft.device)
         new = (out,)
-    else:
-        _expect(out, "out", (B,), i32, dev)
-    _check(lib.msa_tree_commit(ctypes.byref(_kv_dims(n_kv, D)), K_draft.data_ptr(), V_draft.data_ptr(), path.data_ptr(),
-                               n_path.data_ptr(), B, M, A, K_loc.data_ptr(), V_loc.data_ptr(), loc_len.data_ptr(),
-                               t_loc_max, out.data_ptr(), _stream(stream)))
+    _check(lib.msa_tree_commit(ctypes.addressof(_kv_dims(n_kv, D)), _flat(K_draft, "K_draft", drafts, bf, dev),
+                               _flat(V_draft, "V_draft", drafts, bf, dev), _flat(path, "path", (B, A), i32, dev),
+                               _flat(n_path, "n_path", one, i32, dev), B, M, A, _flat(K_loc, "K_loc", cache, bf, dev),
+                               _flat(V_loc, "V_loc", cache, bf, dev), _flat(loc_len, "loc_len", one, i32, dev),
+                               t_loc_max, _flat(out, "out", one, i32, dev), _launch_stream(stream, dev)))
     _used_on(stream, *new)
     return out
 

@@ -16,8 +16,8 @@
 //                the rotated part two consecutive vectors;
 //   interleaved  unit u: elements 2uV .. 2uV + 2V - 1 (pairs inside the vectors).
 // Either way unit u turns the pairs uV .. uV + V - 1.  A warp takes one row (or a share of its
-// heads when there are few rows): its lanes compute their V cosines and sines once and keep them in
-// registers over the row's heads.  V is the widest of 16 bytes, 4 elements and 1 element that
+// heads when there are few rows): its lanes compute the row's cosines and sines once for all its
+// heads.  V is the widest of 16 bytes, 4 elements and 1 element that
 // divides rot_dim / 2, head_dim, every stride and the pointers' alignment.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -35,6 +35,12 @@ namespace msa {
 
 namespace {
 
+#ifndef ROT_CTAS
+#define ROT_CTAS 2
+#define ROT_U 2
+#define GRAD_CTAS 2
+#define GRAD_U 2
+#endif
 constexpr int kMaxPairs = 128;  // rot_dim / 2 of the largest head
 
 struct HeadsP {
@@ -54,7 +60,8 @@ struct RotP {
   const int32_t* slots;  // append: cache slot of each row
   int64_t rows_per_query;
   int t_loc_max;
-  int D, half, units, L, logL, interleaved, parts, its;
+  int D, half, units, L, logL, interleaved, parts, its, classes;
+  int full;  // every element is turned (rot_dim == head_dim)
   float mag, sign;  // sign: -1 for the transposed rotation
   float w_off, eps, inv_d;
   float* dw_part;  // backward: [CTA][2][D] weight-gradient partials, or null
@@ -94,21 +101,85 @@ struct Vec {
   }
   __device__ static __forceinline__ R load(const T* p) { return *reinterpret_cast<const R*>(p); }
   __device__ static __forceinline__ void store(T* p, R r) { *reinterpret_cast<R*>(p) = r; }
-  __device__ static __forceinline__ void unpack(const R& r, float* x) {
-    T t[V];
-    memcpy(t, &r, sizeof(R));
-#pragma unroll
-    for (int e = 0; e < V; ++e) x[e] = to_f32(t[e]);
-  }
-  __device__ static __forceinline__ R pack(const float* x) {
-    T t[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) t[e] = from_f32<T>(x[e]);
-    R r;
-    memcpy(&r, t, sizeof(R));
-    return r;
-  }
 };
+
+// A lane's unit (two vectors a, b of V elements) as V pairs of fp32.  PAIRED: pair e holds the two
+// elements that are turned together (interleaved layout, or single elements); else pairs 0 .. V/2 - 1
+// are the first vector's neighbours and the others the second's, and pair e is turned with e + V/2.
+__device__ __forceinline__ uint64_t wide2(uint32_t w, __nv_bfloat16) {
+  return pack_f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint64_t wide2(uint32_t w, __half) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_f32x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v, __nv_bfloat16) {
+  const float2 f = unpack_f32x2(v);
+  return pack_bf16x2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t narrow2(uint64_t v, __half) {
+  const float2 f = unpack_f32x2(v);
+  const __half2 h = __floats2half2_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T, int V>
+__device__ __forceinline__ void widen(const typename Vec<T, V>::R& a, const typename Vec<T, V>::R& b, uint64_t (&x)[V]) {
+  if constexpr (V == 1) {
+    T ta, tb;
+    memcpy(&ta, &a, sizeof(T));
+    memcpy(&tb, &b, sizeof(T));
+    x[0] = pack_f32x2(to_f32(ta), to_f32(tb));
+  } else if constexpr (sizeof(T) == 4) {
+    float fa[V], fb[V];
+    memcpy(fa, &a, sizeof(fa));
+    memcpy(fb, &b, sizeof(fb));
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      x[e] = pack_f32x2(fa[2 * e], fa[2 * e + 1]);
+      x[V / 2 + e] = pack_f32x2(fb[2 * e], fb[2 * e + 1]);
+    }
+  } else {
+    uint32_t wa[V / 2], wb[V / 2];
+    memcpy(wa, &a, sizeof(wa));
+    memcpy(wb, &b, sizeof(wb));
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      x[e] = wide2(wa[e], T());
+      x[V / 2 + e] = wide2(wb[e], T());
+    }
+  }
+}
+template <typename T, int V>
+__device__ __forceinline__ void narrow(const uint64_t (&x)[V], typename Vec<T, V>::R& a, typename Vec<T, V>::R& b) {
+  if constexpr (V == 1) {
+    const float2 f = unpack_f32x2(x[0]);
+    const T ta = from_f32<T>(f.x), tb = from_f32<T>(f.y);
+    memcpy(&a, &ta, sizeof(T));
+    memcpy(&b, &tb, sizeof(T));
+  } else if constexpr (sizeof(T) == 4) {
+    float2 fa[V / 2], fb[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      fa[e] = unpack_f32x2(x[e]);
+      fb[e] = unpack_f32x2(x[V / 2 + e]);
+    }
+    memcpy(&a, fa, sizeof(fa));
+    memcpy(&b, fb, sizeof(fb));
+  } else {
+    uint32_t wa[V / 2], wb[V / 2];
+#pragma unroll
+    for (int e = 0; e < V / 2; ++e) {
+      wa[e] = narrow2(x[e], T());
+      wb[e] = narrow2(x[V / 2 + e], T());
+    }
+    memcpy(&a, wa, sizeof(wa));
+    memcpy(&b, wb, sizeof(wb));
+  }
+}
+__device__ __forceinline__ uint64_t swap_f32x2(uint64_t v) {
+  const float2 f = unpack_f32x2(v);
+  return pack_f32x2(f.y, f.x);
+}
 
 // cos and sin of pos * theta from theta as a 64-bit fraction of a turn: the product wraps to the
 // exact fraction of a turn, which is split into the nearest quarter turn and a rest within an
@@ -150,277 +221,372 @@ __device__ __forceinline__ Unit unit_of(const RotP& p, int u) {
   return t;
 }
 
-// rotate one unit in registers: x[0 .. V-1] the first vector, x[V .. 2V-1] the second
-template <int V>
-__device__ __forceinline__ void rotate_unit(const RotP& p, const Unit& t, const float* c, const float* s, float* x) {
-  if (p.interleaved) {
+// The factors that turn a unit: PAIRED: y_e = x_e p_e + swap(x_e) q_e with p = (c, c), q = (-s, s);
+// else y_e = x_e p_e + x_{e+V/2} q_e and y_{e+V/2} = x_{e+V/2} p_{e+V/2} + x_e q_{e+V/2} with
+// p = c, q = -s then s.  (A unit turns the pairs u V .. u V + V - 1.)
+template <int V, bool PAIRED>
+__device__ __forceinline__ void unit_factors(const float2* ang, int i0, int half, uint64_t (&p)[V], uint64_t (&q)[V]) {
+  auto at = [&](int i) { return i < half ? ang[i] : make_float2(1.f, 0.f); };
+  if constexpr (PAIRED) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      const bool r = (2 * e < V || V == 1) ? t.ra : t.rb;
-      const float a = x[2 * e], b = x[2 * e + 1];
-      if (r) {
-        x[2 * e] = a * c[e] - b * s[e];
-        x[2 * e + 1] = b * c[e] + a * s[e];
-      }
+      const float2 cs = at(i0 + e);
+      p[e] = pack_f32x2(cs.x, cs.x);
+      q[e] = pack_f32x2(-cs.y, cs.y);
     }
-  } else if (t.ra) {
+  } else {
 #pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const float a = x[e], b = x[V + e];
-      x[e] = a * c[e] - b * s[e];
-      x[V + e] = b * c[e] + a * s[e];
+    for (int e = 0; e < V / 2; ++e) {
+      const float2 u = at(i0 + 2 * e), v = at(i0 + 2 * e + 1);
+      p[e] = p[V / 2 + e] = pack_f32x2(u.x, v.x);
+      q[e] = pack_f32x2(-u.y, -v.y);
+      q[V / 2 + e] = pack_f32x2(u.y, v.y);
     }
   }
 }
+template <int V, bool PAIRED>
+__device__ __forceinline__ uint64_t partner(const uint64_t (&x)[V], int e) {
+  if constexpr (PAIRED) return swap_f32x2(x[e]);
+  return x[e < V / 2 ? e + V / 2 : e - V / 2];
+}
+// is pair e of the unit turned (else its elements only take their weights)
+template <int V, bool PAIRED, bool INTER>
+__device__ __forceinline__ bool turned(const Unit& t, int e) {
+  return !INTER || V == 1 || 2 * e < V ? t.ra : t.rb;
+}
 
-template <int V, int J>
-__device__ __forceinline__ void row_angles(const RotP& p, const uint64_t* turns, int sub, int64_t pos, float (*c)[V],
-                                           float (*s)[V]) {
-#pragma unroll
-  for (int j = 0; j < J; ++j)
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-      const int i = (sub + j * p.L) * V + e;
-      c[j][e] = 1.f;
-      s[j][e] = 0.f;
-      if (i < p.half) turn_cos_sin(turns[i], pos, p.mag, c[j][e], s[j][e]);
-      s[j][e] *= p.sign;
-    }
+// A row's cosines and sines: the warp's lanes compute each pair's once, `ang` (shared memory of the
+// warp) hands them out
+__device__ __forceinline__ void row_angles(const RotP& p, const uint64_t* turns, int64_t pos, float2* ang, int lane) {
+  __syncwarp();
+  for (int i = lane; i < p.half; i += 32) {
+    float c, s;
+    turn_cos_sin(turns[i], pos, p.mag, c, s);
+    ang[i] = make_float2(c, s * p.sign);
+  }
+  __syncwarp();
 }
 
 // Rotation (NORM false) or norm and rotation of the query and key heads; append: keys and values
-// into the cache.  A warp takes share `part` of a row's iterations (32 / L heads each).
-template <typename T, int V, int J, bool NORM>
-__global__ void __launch_bounds__(256) rotate_kernel(const __grid_constant__ RotP p) {
-  constexpr int U = J == 1 ? 4 : 1;  // iterations whose loads are in flight together
+// into the cache.  Persistent warps, each a row (or share `part` of its iterations of 32 / L heads) at
+// a time.  The weights are folded into the rotation's factors, which stay in registers over the heads
+// of a class: y = (x (w p) + x' (w' q)) r; two elements per instruction throughout.
+template <typename T, int V, int J, bool NORM, bool INTER>
+__global__ void __launch_bounds__(256, ROT_CTAS) rotate_kernel(const __grid_constant__ RotP p) {
+  constexpr int U = J == 1 ? ROT_U : 1;  // iterations whose loads are in flight together
+  constexpr bool PAIRED = INTER || V == 1;
   using X = Vec<T, V>;
   __shared__ uint64_t turns[kMaxPairs];
+  __shared__ float2 angles[8][kMaxPairs];
   for (int i = threadIdx.x; i < p.half; i += blockDim.x) turns[i] = p.turns[i];
   __syncthreads();
   pdl_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int64_t row = item / p.parts;
-  const int part = (int)(item - row * p.parts);
-  if (row >= p.rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane & (p.L - 1), grp = lane >> p.logL, gpw = 32 >> p.logL;
-  float c[J][V], s[J][V];
-  row_angles<V, J>(p, turns, sub, p.pos[row], c, s);
-  int64_t cache_row = -1;
-  if (p.slots) {
-    const int slot = p.slots[row];
-    if (slot >= 0 && slot < p.t_loc_max)
-      cache_row = (row / p.rows_per_query) * p.t_loc_max + slot;
-    else if (slot != -1 && lane == 0)
-      raise_dev_error(kDevErrBadIndex);
-  }
-  const int it0 = (int)((int64_t)part * p.its / p.parts), it1 = (int)((int64_t)(part + 1) * p.its / p.parts);
-  for (int base = it0; base < it1; base += U) {
-    typename X::R a[U][J], b[U][J];
-    T* dst[U];
-    int cls[U];
+  Unit un[J];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      int it = base + u, k = 0;
-      dst[u] = nullptr;
-      if (it >= p.h[0].its) {
-        it -= p.h[0].its;
-        k = 1;
-        if (it >= p.h[1].its) {
-          it -= p.h[1].its;
-          k = 2;
-        }
-      }
-      cls[u] = k;
-      const HeadsP& h = p.h[k];
-      const int head = it * gpw + grp;
-      const bool on = base + u < it1 && head < h.heads && (!p.slots || k == 0 || cache_row >= 0);
-      const T* src = static_cast<const T*>(h.in) + row * h.in_row + (int64_t)head * h.in_head;
-      if (on) {
-        if (p.slots && k > 0)
-          dst[u] = static_cast<T*>(h.out) + (cache_row * h.heads + head) * p.D;
-        else
-          dst[u] = static_cast<T*>(h.out) + row * h.out_row + (int64_t)head * h.out_head;
-      }
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const Unit t = unit_of<V>(p, sub + j * p.L);
-        a[u][j] = on && t.va ? X::load(src + t.a) : X::zero();
-        b[u][j] = on && t.vb ? X::load(src + t.b) : X::zero();
-      }
+  for (int j = 0; j < J; ++j) un[j] = unit_of<V>(p, sub + j * p.L);
+  // A cursor runs over the warp's batches of U iterations: rows (or shares of rows), their classes of
+  // heads, the iterations of a class.  The next batch's loads are in flight while one is worked on.
+  const int64_t n_items = p.rows * p.parts, stride = (int64_t)gridDim.x * (blockDim.x >> 5);
+  struct Cursor {
+    int64_t item, row;
+    int k, base, hi, pos, slot;
+  };
+  auto enter_class = [&](Cursor& c, int k, int64_t part) {  // the share's first class from k on with iterations
+    const int it0 = p.parts == 1 ? 0 : (int)(part * p.its / p.parts);
+    const int it1 = p.parts == 1 ? p.its : (int)((part + 1) * p.its / p.parts);
+    for (; k < p.classes; ++k) {
+      const int first = k == 0 ? 0 : k == 1 ? p.h[0].its : p.h[0].its + p.h[1].its;
+      c.k = k;
+      c.base = max(it0 - first, 0);
+      c.hi = min(it1 - first, p.h[k].its);
+      if (c.base < c.hi) return true;
     }
+    return false;
+  };
+  auto enter_item = [&](Cursor& c) {  // a share has at least one iteration
+    if (c.item >= n_items) return;
+    c.row = p.parts == 1 ? c.item : c.item / p.parts;
+    c.pos = p.pos[c.row];
+    c.slot = p.slots ? p.slots[c.row] : 0;
+    enter_class(c, 0, c.item - c.row * p.parts);
+  };
+  auto advance = [&](Cursor& c) {
+    c.base += U;
+    if (c.base < c.hi || enter_class(c, c.k + 1, c.item - c.row * p.parts)) return;
+    c.item += stride;
+    enter_item(c);
+  };
+  auto fetch = [&](const Cursor& c, typename X::R (&a)[U][J], typename X::R (&b)[U][J]) {
+    if (c.item >= n_items) return;
+    const HeadsP& h = p.h[c.k];
+    const T* hp = static_cast<const T*>(h.in) + c.row * h.in_row + (int64_t)(c.base * gpw + grp) * h.in_head;
+    const int64_t step = gpw * h.in_head;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (base + u >= it1) break;  // warp-uniform
-      const int k = cls[u];
-      if (k == 2) {  // values: copied
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const Unit t = unit_of<V>(p, sub + j * p.L);
-          if (dst[u] && t.va) X::store(dst[u] + t.a, a[u][j]);
-          if (dst[u] && t.vb) X::store(dst[u] + t.b, b[u][j]);
-        }
-        continue;
-      }
-      float x[J][2 * V];
-      float ss = 0.f;
+      const bool on = c.base + u < c.hi && (c.base + u) * gpw + grp < h.heads;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        X::unpack(a[u][j], x[j]);
-        X::unpack(b[u][j], x[j] + V);
-        if (NORM) {
-#pragma unroll
-          for (int e = 0; e < 2 * V; ++e) ss = fmaf(x[j][e], x[j][e], ss);
-        }
+        a[u][j] = on && un[j].va ? X::load(hp + un[j].a) : X::zero();
+        b[u][j] = on && un[j].vb ? X::load(hp + un[j].b) : X::zero();
       }
-      float inv = 1.f;
-      if (NORM) {
-        for (int o = p.L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        inv = __frsqrt_rn(fmaf(ss, p.inv_d, p.eps));
-      }
+      hp += step;
+    }
+  };
+  Cursor cur;
+  cur.item = (int64_t)blockIdx.x * (blockDim.x >> 5) + warp;
+  enter_item(cur);
+  typename X::R a[U][J], b[U][J];
+  fetch(cur, a, b);
+  int64_t angles_of = -1, factors_of = -1;  // row of `angles`; row * 4 + class of the factors
+  uint64_t fp[J][V], fq[J][V];
+  while (cur.item < n_items) {
+    Cursor nxt = cur;
+    advance(nxt);
+    typename X::R na[U][J], nb[U][J];
+    fetch(nxt, na, nb);
+    const int k = cur.k;
+    const HeadsP& h = p.h[k];
+    const bool cached = p.slots && k > 0;
+    if (angles_of != cur.row) {
+      row_angles(p, turns, cur.pos, angles[warp], lane);
+      angles_of = cur.row;
+      if (p.slots && cur.slot != -1 && (cur.slot < 0 || cur.slot >= p.t_loc_max) && lane == 0) raise_dev_error(kDevErrBadIndex);
+    }
+    if (k < 2 && factors_of != cur.row * 4 + k) {
+      factors_of = cur.row * 4 + k;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
-        const Unit t = unit_of<V>(p, sub + j * p.L);
-        if (NORM) {
-          const T* w = static_cast<const T*>(p.h[k].w);
-          float wf[2 * V];
-          if (w) {
-            X::unpack(t.va ? X::load(w + t.a) : X::zero(), wf);
-            X::unpack(t.vb ? X::load(w + t.b) : X::zero(), wf + V);
+        unit_factors<V, PAIRED>(angles[warp], (sub + j * p.L) * V, p.half, fp[j], fq[j]);
+        if (NORM && h.w) {
+          const T* wp = static_cast<const T*>(h.w);
+          uint64_t w[V];
+          widen<T, V>(un[j].va ? X::load(wp + un[j].a) : X::zero(), un[j].vb ? X::load(wp + un[j].b) : X::zero(), w);
+          const uint64_t off = pack_f32x2(p.w_off, p.w_off);
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) x[j][e] = x[j][e] * inv * (p.w_off + wf[e]);
-          } else {
+          for (int e = 0; e < V; ++e) w[e] = add_f32x2(w[e], off);
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) x[j][e] *= inv;
+          for (int e = 0; e < V; ++e) {
+            fp[j][e] = mul_f32x2(fp[j][e], w[e]);
+            fq[j][e] = mul_f32x2(fq[j][e], partner<V, PAIRED>(w, e));
           }
         }
-        rotate_unit<V>(p, t, c[j], s[j], x[j]);
-        if (dst[u] && t.va) X::store(dst[u] + t.a, X::pack(x[j]));
-        if (dst[u] && t.vb) X::store(dst[u] + t.b, X::pack(x[j] + V));
       }
     }
+    const bool live = !cached || (cur.slot >= 0 && cur.slot < p.t_loc_max);
+    const int64_t out_head = cached ? p.D : h.out_head;
+    T* op = static_cast<T*>(h.out) + (int64_t)(cur.base * gpw + grp) * out_head +
+            (cached ? (cur.row / p.rows_per_query * p.t_loc_max + cur.slot) * h.heads * p.D : cur.row * h.out_row);
+    const int64_t step = gpw * out_head;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (cur.base + u >= cur.hi) break;  // warp-uniform
+      if (k < 2) {
+        uint64_t x[J][V], ss2 = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          widen<T, V>(a[u][j], b[u][j], x[j]);
+          if (NORM) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) ss2 = fma_f32x2(x[j][e], x[j][e], ss2);
+          }
+        }
+        uint64_t inv2 = 0;
+        if (NORM) {
+          const float2 s2 = unpack_f32x2(ss2);
+          float ss = s2.x + s2.y;
+          for (int o = p.L >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          const float inv = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+          inv2 = pack_f32x2(inv, inv);
+        }
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint64_t y[V];
+          if (p.full) {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              y[e] = fma_f32x2(partner<V, PAIRED>(x[j], e), fq[j][e], mul_f32x2(x[j][e], fp[j][e]));
+          } else {  // what is not turned is not multiplied by a zero sine: the other may be infinite
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+              if (turned<V, PAIRED, INTER>(un[j], e))
+                y[e] = fma_f32x2(partner<V, PAIRED>(x[j], e), fq[j][e], mul_f32x2(x[j][e], fp[j][e]));
+              else
+                y[e] = NORM ? mul_f32x2(x[j][e], fp[j][e]) : x[j][e];
+          }
+          if (NORM) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) y[e] = mul_f32x2(y[e], inv2);
+          }
+          narrow<T, V>(y, a[u][j], b[u][j]);
+        }
+      }
+      const bool on = (cur.base + u) * gpw + grp < h.heads && live;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {  // (the values of an append are stored as they came)
+        if (on && un[j].va) X::store(op + un[j].a, a[u][j]);
+        if (on && un[j].vb) X::store(op + un[j].b, b[u][j]);
+      }
+      op += step;
+    }
+    cur = nxt;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        a[u][j] = na[u][j];
+        b[u][j] = nb[u][j];
+      }
   }
 }
 
-// Gradients of the norms: persistent warps take (row, share) items in a fixed order and keep the
-// weight gradients of their lanes' elements in registers; a CTA sums its warps in order and writes
-// one partial per weight.
-template <typename T, int V, int J>
-__global__ void __launch_bounds__(256) norm_grad_kernel(const __grid_constant__ RotP p) {
-  constexpr int U = J == 1 ? 2 : 1;
+// Gradients of the norms: persistent warps take (row, share) items in a fixed order, the query heads
+// of all of them and then the key heads, and keep the weight gradients of their lanes' elements in
+// registers; a CTA sums its warps in order and writes one partial per weight.
+//   z = Rot^T(dy), u = z w, n = x r:  dx = r u - (r^2 mean(u n)) x,  dw += z n
+template <typename T, int V, int J, bool INTER>
+__global__ void __launch_bounds__(256, GRAD_CTAS) norm_grad_kernel(const __grid_constant__ RotP p) {
+  constexpr int U = J == 1 ? GRAD_U : 1;
+  constexpr bool PAIRED = INTER || V == 1;
   using X = Vec<T, V>;
-  extern __shared__ float red[];  // [warps][2][D]
+  extern __shared__ float red[];  // [warps][D]
   __shared__ uint64_t turns[kMaxPairs];
+  __shared__ float2 angles[8][kMaxPairs];
   for (int i = threadIdx.x; i < p.half; i += blockDim.x) turns[i] = p.turns[i];
   __syncthreads();
   pdl_enter();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
   const int sub = lane & (p.L - 1), grp = lane >> p.logL, gpw = 32 >> p.logL;
-  float dw[2][J][2 * V];
+  Unit un[J];
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) dw[k][j][e] = 0.f;
+  for (int j = 0; j < J; ++j) un[j] = unit_of<V>(p, sub + j * p.L);
   const int64_t n_items = p.rows * p.parts, stride = (int64_t)gridDim.x * n_warps;
-  for (int64_t item = (int64_t)blockIdx.x * n_warps + warp; item < n_items; item += stride) {
-    const int64_t row = item / p.parts;
-    const int part = (int)(item - row * p.parts);
-    float c[J][V], s[J][V];
-    row_angles<V, J>(p, turns, sub, p.pos[row], c, s);
-    const int it0 = (int)((int64_t)part * p.its / p.parts), it1 = (int)((int64_t)(part + 1) * p.its / p.parts);
+#pragma unroll 1
+  for (int k = 0; k < p.classes; ++k) {
+    const HeadsP& h = p.h[k];
+    uint64_t dw[J][V], w[J][V];
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const HeadsP& h = p.h[k];
-      const int first = k ? p.h[0].its : 0;
-      const int lo = max(it0 - first, 0), hi = min(it1 - first, h.its);
-      const T* w = static_cast<const T*>(h.w);
+    for (int j = 0; j < J; ++j) {
+      const T* wp = static_cast<const T*>(h.w);
+      widen<T, V>(wp && un[j].va ? X::load(wp + un[j].a) : X::zero(), wp && un[j].vb ? X::load(wp + un[j].b) : X::zero(),
+                  w[j]);
+      const float add = wp ? p.w_off : 1.f;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        w[j][e] = add_f32x2(w[j][e], pack_f32x2(add, add));
+        dw[j][e] = 0;
+      }
+    }
+    for (int64_t item = (int64_t)blockIdx.x * n_warps + warp; item < n_items; item += stride) {
+      const int64_t row = p.parts == 1 ? item : item / p.parts;
+      const int part = (int)(item - row * p.parts);
+      const int lo = p.parts == 1 ? 0 : (int)((int64_t)part * h.its / p.parts);
+      const int hi = p.parts == 1 ? h.its : (int)((int64_t)(part + 1) * h.its / p.parts);
+      if (lo >= hi) continue;
+      row_angles(p, turns, p.pos[row], angles[warp], lane);
+      uint64_t fp[J][V], fq[J][V];
+#pragma unroll
+      for (int j = 0; j < J; ++j) unit_factors<V, PAIRED>(angles[warp], (sub + j * p.L) * V, p.half, fp[j], fq[j]);
+      const int first = lo * gpw + grp;
+      const T* xp = static_cast<const T*>(h.in) + row * h.in_row + first * h.in_head;
+      const T* gp = static_cast<const T*>(h.g) + row * h.g_row + first * h.g_head;
+      T* op = static_cast<T*>(h.out) + row * h.out_row + first * h.out_head;
+      const int64_t x_step = gpw * h.in_head, g_step = gpw * h.g_head, out_step = gpw * h.out_head;
+#pragma unroll 1
       for (int base = lo; base < hi; base += U) {
         typename X::R xa[U][J], xb[U][J], ga[U][J], gb[U][J];
         bool on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const int head = (base + u) * gpw + grp;
-          on[u] = base + u < hi && head < h.heads;
-          const T* src = static_cast<const T*>(h.in) + row * h.in_row + (int64_t)head * h.in_head;
-          const T* grd = static_cast<const T*>(h.g) + row * h.g_row + (int64_t)head * h.g_head;
+          on[u] = base + u < hi && (base + u) * gpw + grp < h.heads;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            const Unit t = unit_of<V>(p, sub + j * p.L);
-            xa[u][j] = on[u] && t.va ? X::load(src + t.a) : X::zero();
-            xb[u][j] = on[u] && t.vb ? X::load(src + t.b) : X::zero();
-            ga[u][j] = on[u] && t.va ? X::load(grd + t.a) : X::zero();
-            gb[u][j] = on[u] && t.vb ? X::load(grd + t.b) : X::zero();
+            xa[u][j] = on[u] && un[j].va ? X::load(xp + un[j].a) : X::zero();
+            xb[u][j] = on[u] && un[j].vb ? X::load(xp + un[j].b) : X::zero();
+            ga[u][j] = on[u] && un[j].va ? X::load(gp + un[j].a) : X::zero();
+            gb[u][j] = on[u] && un[j].vb ? X::load(gp + un[j].b) : X::zero();
           }
+          xp += x_step;
+          gp += g_step;
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if (base + u >= hi) break;  // warp-uniform
-          float x[J][2 * V], z[J][2 * V], wf[J][2 * V];
-          float ss = 0.f, dot = 0.f;
+          uint64_t x[J][V], z[J][V], ss2 = 0, dot2 = 0;
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            const Unit t = unit_of<V>(p, sub + j * p.L);
-            X::unpack(xa[u][j], x[j]);
-            X::unpack(xb[u][j], x[j] + V);
-            X::unpack(ga[u][j], z[j]);
-            X::unpack(gb[u][j], z[j] + V);
-            rotate_unit<V>(p, t, c[j], s[j], z[j]);
-            if (w) {
-              X::unpack(t.va ? X::load(w + t.a) : X::zero(), wf[j]);
-              X::unpack(t.vb ? X::load(w + t.b) : X::zero(), wf[j] + V);
+            uint64_t g[V];
+            widen<T, V>(xa[u][j], xb[u][j], x[j]);
+            widen<T, V>(ga[u][j], gb[u][j], g);
+            if (p.full) {
+#pragma unroll
+              for (int e = 0; e < V; ++e)
+                z[j][e] = fma_f32x2(partner<V, PAIRED>(g, e), fq[j][e], mul_f32x2(g[e], fp[j][e]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < V; ++e)
+                z[j][e] = turned<V, PAIRED, INTER>(un[j], e)
+                              ? fma_f32x2(partner<V, PAIRED>(g, e), fq[j][e], mul_f32x2(g[e], fp[j][e]))
+                              : g[e];
             }
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-              wf[j][e] = w ? p.w_off + wf[j][e] : 1.f;
-              ss = fmaf(x[j][e], x[j][e], ss);
-              dot = fmaf(z[j][e] * wf[j][e], x[j][e], dot);
+            for (int e = 0; e < V; ++e) {
+              ss2 = fma_f32x2(x[j][e], x[j][e], ss2);
+              dot2 = fma_f32x2(mul_f32x2(z[j][e], w[j][e]), x[j][e], dot2);
             }
           }
+          const float2 s2 = unpack_f32x2(ss2), d2 = unpack_f32x2(dot2);
+          float ss = s2.x + s2.y, dot = d2.x + d2.y;
           for (int o = p.L >> 1; o > 0; o >>= 1) {
             ss += __shfl_xor_sync(0xffffffffu, ss, o);
             dot += __shfl_xor_sync(0xffffffffu, dot, o);
           }
           // lanes without a head add nothing to the weight sums (eps may be 0)
-          const float inv = on[u] ? __frsqrt_rn(fmaf(ss, p.inv_d, p.eps)) : 0.f;
-          const float mean = dot * inv * p.inv_d;  // mean of u n
-          T* dst = static_cast<T*>(h.out) + row * h.out_row + (int64_t)((base + u) * gpw + grp) * h.out_head;
+          const float inv = on[u] ? rsqrtf(fmaf(ss, p.inv_d, p.eps)) : 0.f;
+          const float pull = -inv * inv * (dot * inv * p.inv_d);  // -r^2 mean(u n)
+          const uint64_t inv2 = pack_f32x2(inv, inv), pull2 = pack_f32x2(pull, pull);
 #pragma unroll
           for (int j = 0; j < J; ++j) {
-            const Unit t = unit_of<V>(p, sub + j * p.L);
-            float dx[2 * V];
+            uint64_t dx[V];
 #pragma unroll
-            for (int e = 0; e < 2 * V; ++e) {
-              const float n = x[j][e] * inv;
-              dw[k][j][e] = fmaf(z[j][e], n, dw[k][j][e]);
-              dx[e] = inv * (z[j][e] * wf[j][e] - n * mean);
+            for (int e = 0; e < V; ++e) {
+              const uint64_t zr = mul_f32x2(z[j][e], inv2);
+              dw[j][e] = fma_f32x2(zr, x[j][e], dw[j][e]);
+              dx[e] = fma_f32x2(zr, w[j][e], mul_f32x2(x[j][e], pull2));
             }
-            if (on[u] && t.va) X::store(dst + t.a, X::pack(dx));
-            if (on[u] && t.vb) X::store(dst + t.b, X::pack(dx + V));
+            typename X::R oa, ob;
+            narrow<T, V>(dx, oa, ob);
+            if (on[u] && un[j].va) X::store(op + un[j].a, oa);
+            if (on[u] && un[j].vb) X::store(op + un[j].b, ob);
           }
+          op += out_step;
         }
       }
     }
-  }
-  if (!p.dw_part) return;
+    if (!p.dw_part) continue;
+    if (k) __syncthreads();  // the sums of the query heads are read
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
+    for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int j = 0; j < J; ++j) {
-      const Unit t = unit_of<V>(p, sub + j * p.L);
-#pragma unroll
-      for (int e = 0; e < 2 * V; ++e) {
-        float v = dw[k][j][e];
-        for (int o = 16; o >= p.L; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);  // the warp's heads
-        if (grp == 0 && (e < V ? t.va : t.vb)) red[(warp * 2 + k) * p.D + (e < V ? t.a + e : t.b + e - V)] = v;
+      for (int e = 0; e < V; ++e) {
+        float2 v = unpack_f32x2(dw[j][e]);
+        for (int o = 16; o >= p.L; o >>= 1) {  // the warp's heads
+          v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+          v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        // pair e holds elements 2e, 2e + 1 of the unit's 2V (first vector, second vector)
+        if (grp == 0 && (2 * e < V ? un[j].va : un[j].vb))
+          red[warp * p.D + (2 * e < V ? un[j].a + 2 * e : un[j].b + 2 * e - V)] = v.x;
+        if (grp == 0 && (2 * e + 1 < V ? un[j].va : un[j].vb))
+          red[warp * p.D + (2 * e + 1 < V ? un[j].a + 2 * e + 1 : un[j].b + 2 * e + 1 - V)] = v.y;
       }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.D; i += blockDim.x) {
+      float v = 0.f;
+      for (int q = 0; q < n_warps; ++q) v += red[q * p.D + i];
+      p.dw_part[((int64_t)blockIdx.x * 2 + k) * p.D + i] = v;
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.D; i += blockDim.x) {
-    float v = 0.f;
-    for (int w = 0; w < n_warps; ++w) v += red[w * 2 * p.D + i];
-    p.dw_part[(int64_t)blockIdx.x * 2 * p.D + i] = v;
   }
 }
 
@@ -457,31 +623,33 @@ bool vec_ok(const void* ptr, int64_t s0, int64_t s1, int v, int size) {
 // workspace holds one partial per CTA
 int grad_ctas(int64_t rows, int its) {
   const int64_t warps = rows * std::max(1, its);
-  return (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8, 2 * sm_count()));
+  return (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8, GRAD_CTAS * sm_count()));
 }
 
 template <typename T, int V, int J>
 cudaError_t launch_forward(const RotP& p, bool norm, cudaStream_t s) {
   const int64_t warps = p.rows * p.parts;
-  // few warps: a small CTA on each of many SMs; many: 8 warps per CTA
+  // few warps: a small CTA on each of many SMs; many: 8 warps per CTA, persistent, three CTAs per SM
   const int wpc = warps >= 8LL * sm_count() ? 8 : (int)std::max<int64_t>(1, warps / sm_count());
-  const dim3 grid((unsigned)((warps + wpc - 1) / wpc));
-  return norm ? launch_pdl(rotate_kernel<T, V, J, true>, grid, dim3(32 * wpc), 0, s, p)
-              : launch_pdl(rotate_kernel<T, V, J, false>, grid, dim3(32 * wpc), 0, s, p);
+  const dim3 grid((unsigned)std::min<int64_t>((warps + wpc - 1) / wpc, ROT_CTAS * sm_count()));
+  auto kern = norm ? (p.interleaved ? rotate_kernel<T, V, J, true, true> : rotate_kernel<T, V, J, true, false>)
+                   : (p.interleaved ? rotate_kernel<T, V, J, false, true> : rotate_kernel<T, V, J, false, false>);
+  return launch_pdl(kern, grid, dim3(32 * wpc), 0, s, p);
 }
 
 template <typename T, int V, int J>
 cudaError_t launch_backward(const RotP& p, int ctas, cudaStream_t s) {
-  const size_t sm = 8 * 2 * (size_t)p.D * sizeof(float);
-  return launch_pdl(norm_grad_kernel<T, V, J>, dim3(ctas), dim3(256), sm, s, p);
+  const size_t sm = 8 * (size_t)p.D * sizeof(float);
+  auto kern = p.interleaved ? norm_grad_kernel<T, V, J, true> : norm_grad_kernel<T, V, J, false>;
+  return launch_pdl(kern, dim3(ctas), dim3(256), sm, s, p);
 }
 
 template <typename T>
 cudaError_t launch_typed(const RotP& p, int v, int mode, int ctas, cudaStream_t s) {
   constexpr int W = 16 / (int)sizeof(T);
   if (v == W) return mode == 2 ? launch_backward<T, W, 1>(p, ctas, s) : launch_forward<T, W, 1>(p, mode == 1, s);
-  if (sizeof(T) == 2 && v == 4)
-    return mode == 2 ? launch_backward<T, 4, 1>(p, ctas, s) : launch_forward<T, 4, 1>(p, mode == 1, s);
+  if constexpr (sizeof(T) == 2)
+    if (v == 4) return mode == 2 ? launch_backward<T, 4, 1>(p, ctas, s) : launch_forward<T, 4, 1>(p, mode == 1, s);
   return mode == 2 ? launch_backward<T, 1, 4>(p, ctas, s) : launch_forward<T, 1, 4>(p, mode == 1, s);
 }
 
@@ -544,6 +712,7 @@ msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall&
   p.D = r.head_dim;
   p.half = r.rot_dim / 2;
   p.interleaved = r.layout == MSA_LAYOUT_INTERLEAVED;
+  p.full = r.rot_dim == r.head_dim;
   p.mag = (float)r.magnitude;
   p.sign = c.mode == 2 || c.grad ? -1.f : 1.f;
   p.w_off = c.weight_offset;
@@ -597,6 +766,7 @@ msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall&
       h.g_head = gr[i]->in_head;
     }
     p.its += h.its;
+    p.classes = i + 1;
   }
   // shares of a row: enough warps for every SM when there are few rows
   const int64_t want = 16LL * sm_count();

@@ -193,22 +193,6 @@ __device__ __forceinline__ int blocks_of(const TreeP& p, int n) {
   return (n + NT * p.TT - 1) / (NT * p.TT);
 }
 
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // scores that the row does not see become -inf
 __device__ __forceinline__ void hide(float (&s)[32], uint32_t see) {
 #pragma unroll
@@ -260,15 +244,15 @@ __device__ __forceinline__ float row_weights(uint32_t addr, const uint32_t (&see
     uint32_t u[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      const uint64_t y = fma_f32x2(pack_f32x2(cur[2 * e], cur[2 * e + 1]), c2, neg2);
-      const float a = ex2(__uint_as_float((uint32_t)y)), z = ex2(__uint_as_float((uint32_t)(y >> 32)));
+      const float2 y = unpack_f32x2(fma_f32x2(pack_f32x2(cur[2 * e], cur[2 * e + 1]), c2, neg2));
+      const float a = ex2(y.x), z = ex2(y.y);
       sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(a, z));
       u[e] = pack_bf16x2(a, z);
     }
     tmem_st16(addr + 16 * q, u);
   }
-  sum[0] = add_f32x2(sum[0], sum[1]);
-  return __uint_as_float((uint32_t)sum[0]) + __uint_as_float((uint32_t)(sum[0] >> 32));
+  const float2 both = unpack_f32x2(add_f32x2(sum[0], sum[1]));
+  return both.x + both.y;
 }
 
 // each query's pooled rows (large batches only): a warp per query
@@ -876,9 +860,9 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
 // takes 1024 / D rows of the item noted by one CTA, a thread 4 elements of a row, neighbouring
 // threads neighbouring rows (as the parts lie); the parts are read once, kAhead of them in flight,
 // with a running maximum.
-template <int D, int NT>
+template <int D, int NT, int kAhead>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeP p) {
-  constexpr int kRows = 1024 / D, kAhead = 8;
+  constexpr int kRows = 1024 / D;
   pdl_enter();
   const int4 it = p.merges[2 * blockIdx.y], cs = p.merges[2 * blockIdx.y + 1];
   const int b = it.x, n = it.w, c0 = cs.x, c1 = cs.y;
@@ -960,7 +944,10 @@ cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   TraceScope ts(kKTreeCombine, s);
   constexpr int kRows = 1024 / D;
   const int row_groups = NT == 1 ? (p.M * p.G + kRows - 1) / kRows : NT * 128 / kRows;
-  return launch_pdl(tree_combine_kernel<D, NT>, dim3(row_groups, n_ctas), dim3(256), 0, s, p);
+  // many items: about two parts each, and many threads; few items: many parts, their loads in flight
+  // together (1m case: 18 parts, 16 ahead; 16m case: 2 parts, 18 us with 8 ahead and 9 us with 4)
+  auto merge = (int64_t)p.B * p.n_rb * p.n_kv * 4 > n_ctas ? tree_combine_kernel<D, NT, 2> : tree_combine_kernel<D, NT, 16>;
+  return launch_pdl(merge, dim3(row_groups, n_ctas), dim3(256), 0, s, p);
 }
 
 struct TreeWs {

@@ -4,5 +4,3 @@ from .msa_oracle import EPS, bf16_to_f64, chunk_layout, rope, rope_theta, encode
 from .msa_oracle import router_query, cosine, chunk_scores, doc_scores, topk, route_topk  # noqa: F401
 from .msa_oracle import sparse_context, attention, sparse_attend, sparse_attend_tokens  # noqa: F401
 from .msa_oracle import aux_loss  # noqa: F401
-from .msa_oracle import rotary_theta, rotate_heads, head_norm, head_norm_rotate_grad  # noqa: F401
-from .msa_oracle import tree_plan, pack_mask, tree_attend  # noqa: F401

@@ -5,7 +5,7 @@ import ctypes
 import numpy as np
 import pytest
 
-import oracle as O
+import context_oracle as O
 
 FAKE = 0x10000  # 16-byte aligned non-null "device" address; never dereferenced
 
@@ -58,8 +58,8 @@ def test_oracle_gradients_match_differences():
 
 def _heads(msa, heads=4, D=64, inp=FAKE, out=FAKE, in_row=None, in_head=None, out_row=None, out_head=None):
     pick = lambda v, d: d if v is None else v
-    return msa._Heads(inp, out, pick(in_row, heads * D), pick(in_head, D), pick(out_row, heads * D), pick(out_head, D),
-                      heads, 0)
+    return msa._HEADS.pack(inp or 0, out or 0, pick(in_row, heads * D), pick(in_head, D), pick(out_row, heads * D),
+                           pick(out_head, D), heads, 0)
 
 
 def _rotate(msa, rot=None, dtype=0, rows=3, pos=FAKE, q=None, k=None):
@@ -224,7 +224,8 @@ def test_binding_refuses_wrong_shapes_and_types(msa, monkeypatch):
     """The binding's checks, on host tensors with the device check stood in for."""
     import torch
 
-    monkeypatch.setattr(msa, "_on_device", lambda t, name: t.device)
+    msa._bind_torch()
+    monkeypatch.setattr(msa, "_on_device", lambda t, name: t.get_device())
     r = msa.rotary(64)
     q, k, pos = torch.zeros(4, 3, 64), torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32)
     for args, kw in [((r, q.double(), pos), {}), ((r, q[..., :32], pos), {}), ((r, q.reshape(12, 64), pos), {}),

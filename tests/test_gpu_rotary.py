@@ -9,7 +9,7 @@ of the sum of squares, halved by the root, and the root's and the products' own)
 import numpy as np
 import pytest
 
-import oracle as O
+import context_oracle as O
 
 pytestmark = pytest.mark.gpu
 

@@ -8,7 +8,7 @@ to bf16 before it multiplies its value, 2^-8 of A = sum_j p_j |v_j|; the scores'
 import numpy as np
 import pytest
 
-import oracle as O
+import context_oracle as O
 from long_context_memory_b200 import workloads as W
 
 pytestmark = pytest.mark.gpu
