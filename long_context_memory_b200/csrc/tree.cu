@@ -117,7 +117,11 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 //
 // The rows that share a KV head (drafts x GQA group) fill the 128 rows of tcgen05 tiles: a row tile
 // is TT = 128 / G drafts with their G heads, a CTA takes NT row tiles at once (two when one does not
-// hold all drafts), so K and V cross HBM once per 256 rows and each key tile of 128 keys costs
+// hold all drafts), so K and V cross HBM once per 256 rows.  Two streams of scores, weights and
+// outputs run beside each other, so that the tensor cores and one stream's softmax overlap the
+// other's softmax: with two row tiles a stream is a row tile (each key tile goes through both); with
+// one, the streams take the key tiles in turn, each with a maximum, sum and output of its own,
+// joined at the item's end.  A stream's step costs
 //   S = Q K^T   (tcgen05, operands in shared memory, fp32 scores in tensor memory),
 //   P = exp2(S c - m)   (one thread per row, scores and weights in registers),
 //   O += P V    (tcgen05, P bf16 in tensor memory over S, V in shared memory, O in tensor memory).
@@ -141,12 +145,12 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // fill them: whatever stands in the rows behind a sequence, and in drafts that nobody sees, never
 // reaches a product.
 //
-// Warps: 4 NT softmax warps (a thread per row), one producer (item headers, document tables, TMA),
+// Warps: 2 x 4 softmax warps (a stream each, a thread per row), one producer (item headers, document tables, TMA),
 // one MMA issuer.  One CTA per SM (its ring fills the shared memory).
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;        // keys per tile, rows per row tile
 constexpr int kMaxRing = 6;
-constexpr int kSmallB = 64;       // queries whose tile counts every CTA computes itself
+constexpr int kSmallB = 32;       // queries whose tile counts every CTA computes itself
 constexpr float kSlack = 8.f;
 constexpr int kTmemCols = 512;    // scores 2 x 128, outputs 2 x 128
 
@@ -165,7 +169,7 @@ struct TreeP {
   int32_t* sel;      // [B] pooled rows of each query's documents (B > kSmallB)
   float* part_o;     // [2 N][D / 4][NT * 128][4] unnormalised (a warp's rows side by side)
   float* part_ml;    // [2 N][NT * 128][2] reference maximum, sum
-  int B, M, W, n_q, n_kv, G, TT, n_rb, t_loc_max, n_docs, n_chunks, k, ring;
+  int B, M, W, n_q, n_kv, G, TT, n_rb, t_loc_max, n_docs, n_chunks, k, ring, pad;
   float scale_log2;
 };
 
@@ -294,18 +298,19 @@ __device__ __forceinline__ Cover cover_of(int n) {
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __grid_constant__ TreeMaps maps,
+__global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_constant__ TreeMaps maps,
                                                                        const __grid_constant__ TreeP p) {
   constexpr int DB = D / 64;            // 64-element blocks of a head
   constexpr int kBlk = kTile * 128;     // bytes of one block of a 128-row tile
   constexpr int kTB = DB * kBlk;        // bytes of a tile
-  constexpr int kThreads = 128 * NT + 64;
-  constexpr int kSoftWarps = 4 * NT;
+  constexpr int kThreads = 320;
+  constexpr int kSoftWarps = 8;
   // (declared with the alignment that is sure behind the statically sized part; a stricter one would
   // be taken on trust and fold the rounding below away)
   extern __shared__ __align__(16) uint8_t sm_raw[];
   __shared__ uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-  __shared__ uint64_t qfull, qempty, sfull[2], pready[2], pvdone[2], ofree[2], hfull[2], hempty[2], drained;
+  __shared__ uint64_t qfull, qempty, sfull[2], pready[2], pvdone[2], ofree[2], joined, taken, hfull[2], hempty[2], drained;
+  __shared__ float2 state[NT == 1 ? kTile : 1];  // one row tile: stream 1's reference maximum and sum of each row
   __shared__ int hdr[2][kHWords];
   __shared__ int q_sel[kSmallB], q_loc[kSmallB], q_n[kSmallB];  // small batches: pooled rows, local rows, drafts
   __shared__ long long warp_sum[kThreads / 32];
@@ -319,6 +324,10 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
   uint8_t* vs = ks + p.ring * kTB;        // [ring] value tiles
   int* tab = reinterpret_cast<int*>(vs + p.ring * kTB);  // the query's documents: [k + 1] first key, [k] first row
 
+  if (qs - sm_raw > p.pad) {  // the tiles would not fit where the launch put them
+    if (threadIdx.x == 0) raise_dev_error(kDevErrBadIndex);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < p.ring; ++i) {
@@ -330,6 +339,8 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     mbar_init(&qfull, 1);
     mbar_init(&qempty, 1);
     mbar_init(&drained, 1);
+    mbar_init(&joined, 4);
+    mbar_init(&taken, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
       mbar_init(&pready[i], 4);
@@ -685,8 +696,8 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
         const uint64_t v = vd + (uint64_t)(vs_st * (kTB / 16));
 #pragma unroll
         for (int s = 0; s < kTile / 16; ++s)
-          umma_bf16_ts(tmem + 256 + i * 128, tmem + slot * 128 + s * 8, v + s * (2048 / 16), idesc_o, !first || s > 0);
-        umma_commit(&pvdone[i]);
+          umma_bf16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + s * 8, v + s * (2048 / 16), idesc_o, !first || s > 0);
+        umma_commit(&pvdone[slot]);
         if (i == NT - 1) {
           umma_commit(&vempty[vs_st]);
           if (++vs_st == p.ring) {
@@ -710,7 +721,7 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
           if (t + 1 == T) umma_commit(&qempty);  // every product with these queries is issued
           for (int i = 0; i < NT && ok; ++i) {
             if (t == 0 && j > 0) ok = mbar_wait_short(&ofree[i], (j - 1) & 1, &abort_flag);
-            if (ok) ok = weigh(i, x, t == 0);
+            if (ok) ok = weigh(i, x, NT == 1 ? t < 2 : t == 0);  // the stream's first tile of the item
             if (NT == 2 && ok && t + 1 < T) ok = scores(i, x + 1);
           }
         }
@@ -727,19 +738,21 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
     // =======================================================================
     // softmax: thread r of a row tile owns row r (draft t0 + r / G, head r % G)
     // =======================================================================
-    const int i = warp >> 2;                        // row tile
+    const int str = warp >> 2;                      // stream
+    const int i = NT == 1 ? 0 : str;                // row tile
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const int r = (warp & 3) * 32 + lane;
-    const uint32_t o_addr = tmem + 256 + i * 128 + lane_base;
+    const uint32_t s_addr = tmem + str * 128 + lane_base, o_addr = tmem + 256 + str * 128 + lane_base;
     // rows behind a query's last block in use belong to no item: zeros
     for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
       const int t1 = blocks_of<NT>(p, small ? q_n[b] : drafts_of(p, b)) * NT * p.TT;
       if (t1 < p.M) {
         uint4* z = reinterpret_cast<uint4*>(p.out + ((size_t)b * p.M + t1) * p.n_q * D);
-        for (int e = tid; e < (p.M - t1) * p.n_q * (D / 8); e += 128 * NT) z[e] = make_uint4(0, 0, 0, 0);
+        for (int e = tid; e < (p.M - t1) * p.n_q * (D / 8); e += 32 * kSoftWarps) z[e] = make_uint4(0, 0, 0, 0);
       }
     }
-    uint32_t x = 0;
+    uint32_t x = 0;  // key tiles of the CTA before this item
+    uint32_t n = 0;  // tiles of this stream so far: the phase of its barriers
     bool ok = true;
     for (int j = 0; ok; ++j) {
       const int hb = j & 1;
@@ -747,18 +760,19 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
       const int* h = hdr[hb];
       const int b = h[kHb];
       if (b < 0) break;
-      const int hk = h[kHhk], sel = h[kHsel], L = h[kHL], n = h[kHn], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
+      const int hk = h[kHhk], sel = h[kHsel], L = h[kHL], n_use = h[kHn], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
                 hi = h[kHhi], part = h[kHslot];
       const int rt = r / p.G, g = r - rt * p.G;
       const int t_row = h[kHt0] + i * p.TT + rt;
-      const bool in_use = rt < p.TT && t_row < n;
+      const bool in_use = rt < p.TT && t_row < n_use;
       const int32_t* mk = p.mask + ((size_t)b * p.M + (in_use ? t_row : 0)) * p.W;
       float m_ref = -INFINITY, l = 0.f;
-      for (int t = lo; t < hi; ++t, ++x) {
+      const int step = NT == 1 ? 2 : 1, t_first = NT == 1 ? lo + ((str - (int)x) & 1) : lo;
+      for (int t = t_first; t < hi; t += step, ++n) {
         // ---- the keys of the tile that this row sees ----
         uint32_t see[4];
         const bool drafts = t >= Tc + Tl;
-        const int left = t < Tc ? sel - t * kTile : drafts ? n - (t - Tc - Tl) * kTile : L - (t - Tc) * kTile;
+        const int left = t < Tc ? sel - t * kTile : drafts ? n_use - (t - Tc - Tl) * kTile : L - (t - Tc) * kTile;
         const int w0 = (t - Tc - Tl) * (kTile / 32);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -767,19 +781,17 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
           if (drafts) see[q] &= in_use && w0 + q < p.W ? (uint32_t)mk[w0 + q] : 0u;
         }
         const bool all = __all_sync(0xffffffffu, (see[0] & see[1] & see[2] & see[3]) == ~0u);
-        const uint32_t slot = NT == 1 ? (x & 1) : i;
-        const uint32_t s_addr = tmem + slot * 128 + lane_base;
-        if (!warp_wait_short(&sfull[slot], (NT == 1 ? x >> 1 : x) & 1, &abort_flag)) {
+        if (!warp_wait_short(&sfull[str], n & 1, &abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const float m_new = (all ? row_max<false>(s_addr, see) : row_max<true>(s_addr, see)) * p.scale_log2;
-        const bool grow = m_new > m_ref + kSlack || (t == lo && m_new > m_ref);
+        const bool grow = m_new > m_ref + kSlack || (t == t_first && m_new > m_ref);
         const bool need = grow && l > 0.f;
         const bool any = __any_sync(0xffffffffu, need);
         if (any) {  // O holds products with weights of the old reference: rescale
-          if (!warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) {
+          if (!warp_wait_short(&pvdone[str], (n - 1) & 1, &abort_flag)) {
             ok = false;
             break;
           }
@@ -803,37 +815,76 @@ __global__ void __launch_bounds__(128 * NT + 64, 1) tree_attend_kernel(const __g
         tmem_st_wait();
         // the products of the tile before have ended when those of this one may start: one phase of
         // pvdone is outstanding at a time
-        if (t > lo && !any && !warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) {
+        if (t > t_first && !any && !warp_wait_short(&pvdone[str], (n - 1) & 1, &abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&pready[slot]);
+        if (lane == 0) mbar_arrive(&pready[str]);
       }
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(&hempty[hb]);
-      if (!warp_wait_short(&pvdone[i], (x - 1) & 1, &abort_flag)) break;
+      x += hi - lo;
+      if (t_first < hi && !warp_wait_short(&pvdone[str], (n - 1) & 1, &abort_flag)) break;
+      // the factors of the streams' outputs in this row's (f of a stream without keys is 0, whatever
+      // its output holds)
+      float f0 = 1.f, f1 = 0.f;
+      if (NT == 1) {  // stream 1 hands its state over, stream 0 writes the item
+        if (str == 1) {
+          if (j > 0 && !warp_wait_short(&taken, (j - 1) & 1, &abort_flag)) break;
+          state[r] = make_float2(m_ref, l);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&joined);
+          continue;
+        }
+        if (!warp_wait_short(&joined, j & 1, &abort_flag)) break;
+        const float2 z = state[r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken);
+        const float m0 = m_ref, l0 = l;
+        m_ref = fmaxf(m0, z.x);
+        f0 = m0 == -INFINITY ? 0.f : ex2(m0 - m_ref);
+        f1 = z.x == -INFINITY ? 0.f : ex2(z.x - m_ref);
+        l = f0 * l0 + f1 * z.y;
+      }
       tc_fence_after();
       const bool some = in_use && l != 0.f;  // a NaN sum is kept
       const bool row_out = rt < p.TT && t_row < p.M;
-      const float inv = 1.f / l;
+      if (part < 0) {
+        f0 *= 1.f / l;
+        f1 *= 1.f / l;
+      }
       __nv_bfloat16* out = p.out + (((size_t)b * p.M + t_row) * p.n_q + (size_t)hk * p.G + g) * D;
       float* po = p.part_o + ((size_t)max(part, 0) * (D / 4) * (NT * 128) + i * 128 + r) * 4;
 #pragma unroll 1
       for (int c = 0; c < D; c += 32) {
         float o[32];
         tmem_ld32(o_addr + c, o);
-        tmem_ld_wait_for(o);
+        if (NT == 1) {
+          float o1[32];
+          tmem_ld32(o_addr + 128 + c, o1);
+          tmem_ld_wait_for(o);
+          tmem_ld_wait_for(o1);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = (f0 == 0.f ? 0.f : o[e] * f0) + (f1 == 0.f ? 0.f : o1[e] * f1);
+        } else {
+          tmem_ld_wait_for(o);
+          if (part < 0) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= f0;
+          }
+        }
         if (part < 0) {
           if (row_out) {
 #pragma unroll
             for (int e = 0; e < 32; e += 8) {
               uint4 v = make_uint4(0, 0, 0, 0);
               if (some)
-                v = make_uint4(pack_bf16x2(o[e] * inv, o[e + 1] * inv), pack_bf16x2(o[e + 2] * inv, o[e + 3] * inv),
-                               pack_bf16x2(o[e + 4] * inv, o[e + 5] * inv), pack_bf16x2(o[e + 6] * inv, o[e + 7] * inv));
+                v = make_uint4(pack_bf16x2(o[e], o[e + 1]), pack_bf16x2(o[e + 2], o[e + 3]),
+                               pack_bf16x2(o[e + 4], o[e + 5]), pack_bf16x2(o[e + 6], o[e + 7]));
               *reinterpret_cast<uint4*>(out + c + e) = v;
             }
           }
@@ -929,16 +980,24 @@ template <int D, int NT>
 cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   const int tile = D / 64 * kTile * 128;
   const size_t tables = (size_t)2 * (p.k + 1) * sizeof(int);
-  constexpr size_t kDyn = 227 * 1024 - 1344;  // less the statically sized part
-  p.ring = (int)std::min<size_t>(kMaxRing, (kDyn - 1024 - tables - NT * tile) / (2 * tile));
-  const size_t smem = 1024 + (size_t)(NT + 2 * p.ring) * tile + tables;
+  // what aligning the tiles to 1 KB costs: the dynamic part begins behind the system's 1 KB and the
+  // statically sized part (the kernel checks that this holds)
   auto kern = tree_attend_kernel<D, NT>;
-  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), (int)kDyn);
+  static const size_t fixed = [&] {
+    cudaFuncAttributes a{};
+    return cudaFuncGetAttributes(&a, kern) == cudaSuccess ? (a.sharedSizeBytes + 15) / 16 * 16 : (size_t)0;
+  }();
+  if (fixed == 0) return cudaErrorUnknown;
+  const size_t room = 227 * 1024 - fixed;
+  p.pad = (int)((1024 - (1024 + fixed) % 1024) % 1024);
+  p.ring = (int)std::min<size_t>(kMaxRing, (room - p.pad - tables - NT * tile) / (2 * tile));
+  const size_t smem = p.pad + (size_t)(NT + 2 * p.ring) * tile + tables;
+  cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), (int)room);
   if (e != cudaSuccess) return e;
   const int n_ctas = sm_count();
   {
     TraceScope ts(kKTreeAttend, s);
-    e = launch_pdl(kern, dim3(n_ctas), dim3(128 * NT + 64), smem, s, maps, p);
+    e = launch_pdl(kern, dim3(n_ctas), dim3(320), smem, s, maps, p);
     if (e != cudaSuccess) return e;
   }
   TraceScope ts(kKTreeCombine, s);
