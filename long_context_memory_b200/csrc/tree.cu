@@ -137,13 +137,13 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // CTA shares with its neighbours leave partial results and a note for tree_combine_kernel, which
 // merges them.
 //
-// A tile's rows arrive by TMA boxes of 128, 32, 8 and 1 rows.  A box costs the TMA unit about 55
-// cycles and 2.3 per row of 128 bytes (measured), so a run of rows is covered by equal boxes whose
-// last one overlaps the one before (the same bytes twice) rather than by ever smaller ones; a box
-// may start at any row of the tile, since the 128-byte swizzle goes by the address.  Only rows that
-// some draft sees are copied, into a ring whose V slots start as zeros where a first copy does not
-// fill them: whatever stands in the rows behind a sequence, and in drafts that nobody sees, never
-// reaches a product.
+// A tile's rows arrive by TMA boxes.  A box costs the TMA unit about 55 cycles and 2.3 per row of
+// 128 bytes (measured), so a document's run of rows is covered by at most two boxes, of the largest
+// power of two that is not longer, the second one moved back to end with the run (the rows where
+// they overlap arrive twice, the same bytes); a box may start at any row of the tile, since the
+// 128-byte swizzle goes by the address.  Values are copied only where some draft sees them, into a
+// ring that starts as zeros: whatever stands in the rows behind a sequence, and in drafts that
+// nobody sees, never reaches a product.  (A key too many does no harm: its score is replaced.)
 //
 // Warps: 2 x 4 softmax warps (a stream each, a thread per row), one producer (item headers, document tables, TMA),
 // one MMA issuer.  One CTA per SM (its ring fills the shared memory).
@@ -154,18 +154,22 @@ constexpr int kSmallB = 32;       // queries whose tile counts every CTA compute
 constexpr float kSlack = 8.f;
 constexpr int kTmemCols = 512;    // scores 2 x 128, outputs 2 x 128
 
-constexpr int kBoxRows[4] = {1, 8, 32, 128};
+constexpr int kTailRows[4] = {1, 8, 32, 128};
 
 struct TreeMaps {
   CUtensorMap q;
-  // [K, V][box rows]: kBoxRows for the pooled rows and the local cache, 1 and 8 rows of drafts
-  CUtensorMap bar[2][3], loc[2][4], draft[2][2];
+  CUtensorMap bar[2][7];           // [K, V] pooled rows: boxes of 1, 2, 4 .. 64 rows
+  CUtensorMap k_loc, k_draft;      // 128 rows
+  CUtensorMap v_loc[4], v_draft[2];  // 1, 8, 32 and 128 rows; 1 and 8
 };
 
 struct TreeP {
   const int32_t *mask, *n_draft, *loc_len, *chunk_off, *topk_idx;
   __nv_bfloat16* out;
-  int4* merges;      // [N][2] item cut by CTA c's begin: query, first draft, KV head, drafts | first and last CTA, first part's slot
+  // [2] per item (few items) or per CTA (many): query (-1: nothing to merge), first draft, KV head,
+  // drafts | first and last CTA, first part's slot
+  int4* merges;
+  int by_item;
   int32_t* sel;      // [B] pooled rows of each query's documents (B > kSmallB)
   float* part_o;     // [2 N][D / 4][NT * 128][4] unnormalised (a warp's rows side by side)
   float* part_ml;    // [2 N][NT * 128][2] reference maximum, sum
@@ -284,15 +288,21 @@ __device__ __forceinline__ int divide(long long a, long long b) {  // floor(a / 
   return (a | b) >> 32 ? (int)(a / b) : (int)((uint32_t)a / (uint32_t)b);
 }
 
-// boxes that cover a run of n rows: of the largest size (1, 8, 32) that is not longer than the run,
-// the last one moved back to end with it
+// boxes of one size that cover a run of n <= 128 rows, the last one moved back to end with it
 struct Cover {
   int size, count, level;
 };
-__device__ __forceinline__ Cover cover_of(int n) {
+__device__ __forceinline__ Cover cover_doc(int n) {  // sizes 1, 2, 4 .. 64: at most two boxes
   Cover c;
-  c.level = n >= 32 ? 2 : n >= 8 ? 1 : 0;
-  c.size = n >= 32 ? 32 : n >= 8 ? 8 : 1;
+  c.level = min(6, 31 - __clz(max(n, 1)));
+  c.size = 1 << c.level;
+  c.count = n <= 0 ? 0 : n == c.size ? 1 : 2;
+  return c;
+}
+__device__ __forceinline__ Cover cover_tail(int n) {  // sizes 1, 8, 32, 128
+  Cover c;
+  c.level = n >= 128 ? 3 : n >= 32 ? 2 : n >= 8 ? 1 : 0;
+  c.size = c.level == 3 ? 128 : c.level == 2 ? 32 : c.level == 1 ? 8 : 1;
   c.count = (n + c.size - 1) / c.size;
   return c;
 }
@@ -364,19 +374,24 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
   const uint32_t tmem = tmem_slot;
   pdl_enter();
 
-  // ---- the line of tiles: every CTA counts it (small batches: with everything in shared memory) ----
+  // ---- the line of tiles: every CTA counts it, for small batches in shared memory; meanwhile the
+  // softmax warps clear the value ring (a tile need not fill its slot) ----
   const bool small = p.B <= kSmallB;
-  if (small) {
-    if (tid < p.B) {
-      q_n[tid] = drafts_of(p, tid);
-      q_loc[tid] = local_of(p, tid);
+  if (warp < kSoftWarps) {
+    for (int i = tid; i < p.ring * (kTB / 16); i += 32 * kSoftWarps) reinterpret_cast<uint4*>(vs)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  } else if (small) {
+    const int u0 = tid - 32 * kSoftWarps;  // 64 threads
+    if (u0 < p.B) {
+      q_n[u0] = drafts_of(p, u0);
+      q_loc[u0] = local_of(p, u0);
     }
     const int pairs = p.B * p.k;
-    for (int i0 = tid; i0 < pairs; i0 += 4 * kThreads) {  // four documents of a thread in flight
-      int rows[4];
+    for (int i0 = u0; i0 < pairs; i0 += 8 * 64) {  // eight documents of a thread in flight
+      int rows[8];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int i = i0 + u * kThreads;
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * 64;
         rows[u] = -1;
         if (i < pairs) {
           const int doc = p.topk_idx[i];
@@ -385,11 +400,11 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         }
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (rows[u] > 0) atomicAdd(&q_sel[(i0 + u * kThreads) / p.k], rows[u]);
+      for (int u = 0; u < 8; ++u)
+        if (rows[u] > 0) atomicAdd(&q_sel[(i0 + u * 64) / p.k], rows[u]);
     }
-    __syncthreads();
   }
+  __syncthreads();
   auto query = [&](int b, int& sel, int& L, int& n) {
     n = small ? q_n[b] : drafts_of(p, b);
     L = small ? q_loc[b] : local_of(p, b);
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
     bool fresh = true, listed = false;  // b is new; its documents are in the table
     int L = 0, n = 0, sel = 0, T = 0;
     int *first_key = tab, *first_row = tab + p.k + 1;
-    if (lane == 0) p.merges[2 * blockIdx.x].x = -1;
+    if (lane == 0 && !p.by_item) p.merges[2 * blockIdx.x].x = -1;
     while (ok) {
       const int hb = n_items & 1;
       if (n_items >= 2 && !warp_wait_short(&hempty[hb], ((n_items >> 1) - 1) & 1, &abort_flag)) {
@@ -504,22 +519,15 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           for (int d = 0; d < DB; ++d)
             tma_load_4d(qs + i * kTB + d * kBlk, &maps.q, &qfull, d * 64, hk * p.G, t0 + i * p.TT, b);
       }
-      if (lo > 0 && n_items == 0 && lane == 0) {
-        // the item began in an earlier CTA: the first CTA that it reaches notes it for the merge
-        const long long w0 = w - lo;  // tile w is in the CTA floor(((w + 1) N - 1) / W)
-        const int ca = divide((w0 + 1) * n_act - 1, total), cz = divide((w0 + T) * n_act - 1, total);
-        if (ca + 1 == (int)blockIdx.x) {
-          p.merges[2 * blockIdx.x + 1] = make_int4(ca, cz, 2 * ca + (begin_of(ca) == w0 ? 0 : 1), 0);
-          p.merges[2 * blockIdx.x] = make_int4(b, t0, hk, n);
-        }
-      }
+      const bool first = n_items == 0;
       ++n_items;
       for (int t = lo; t < hi && ok; ++t, ++x) {
         const int c0 = t * kTile, j0 = (t - Tc) * kTile, d0 = (t - Tc - Tl) * kTile;
         const int kind = t < Tc ? 0 : t < Tc + Tl ? 1 : 2;  // pooled rows, local rows, drafts
-        int rows, boxed;         // rows that the tile holds; rows that its boxes bring
-        int doc0 = 0;            // kind 0: the first document with keys in the tile
-        uint32_t bits = 0;       // kind 2, lane < 16: drafts d0 + 8 lane .. that some draft of the query sees
+        int rows, k_rows;   // rows of the tile; rows that its key and value boxes bring
+        int v_rows;
+        int doc0 = 0;       // kind 0: the first document with keys in the tile
+        uint32_t bits = 0;  // kind 2, lane < 16: drafts d0 + 8 lane .. that some draft of the query sees
         if (kind == 0) {
           if (!listed) {  // the query's documents: first key (a running sum) and first pooled row of each
             const int each = (p.k + 31) / 32;
@@ -566,17 +574,17 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
             const int mid = (doc0 + z + 1) >> 1;
             if (first_key[mid] <= c0) doc0 = mid; else z = mid - 1;
           }
-          boxed = 0;
+          int boxed = 0;
           for (int r = doc0 + lane; r < p.k && first_key[r] < c0 + rows; r += 32) {
-            const int run = min(first_key[r + 1], c0 + rows) - max(first_key[r], c0);
-            const Cover c = cover_of(max(run, 0));
+            const Cover c = cover_doc(min(first_key[r + 1], c0 + rows) - max(first_key[r], c0));
             boxed += c.size * c.count;
           }
-          boxed = __reduce_add_sync(0xffffffffu, boxed);
+          k_rows = v_rows = __reduce_add_sync(0xffffffffu, boxed);
         } else if (kind == 1) {
           rows = min(kTile, L - j0);
-          const Cover c = cover_of(rows);
-          boxed = rows == kTile ? kTile : c.size * c.count;
+          const Cover c = cover_tail(rows);
+          k_rows = kTile;
+          v_rows = c.size * c.count;
         } else {
           uint32_t seen[4] = {0, 0, 0, 0};
           for (int r = lane; r < n; r += 32) {
@@ -594,7 +602,8 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
             bits |= (lane >> 2) == q ? seen[q] >> (8 * (lane & 3)) & 0xFFu : 0u;
             rows += __popc(seen[q]);
           }
-          boxed = rows;
+          k_rows = kTile;
+          v_rows = rows;
         }
         for (int kv = 0; kv < 2; ++kv) {
           uint64_t* fullb = (kv ? vfull : kfull) + st;
@@ -603,41 +612,43 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
             ok = false;
             break;
           }
-          if (kv && x < (uint32_t)p.ring && rows < kTile) {  // a slot's first use that leaves rows out
-            for (int i = lane; i < kTB / 16; i += 32) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive_expect_tx(fullb, boxed * D * 2);
+          if (lane == 0) mbar_arrive_expect_tx(fullb, (kv ? v_rows : k_rows) * D * 2);
           __syncwarp();
-          if (kind == 0) {
-            for (int r = doc0 + lane; r < p.k && first_key[r] < c0 + rows; r += 32) {
-              const int a = max(first_key[r], c0), run = min(first_key[r + 1], c0 + rows) - a;
-              if (run <= 0) continue;
-              const Cover c = cover_of(run);
-              const int src = first_row[r] + (a - first_key[r]);
-              for (int i = 0; i < c.count; ++i) {
-                const int o = min(i * c.size, run - c.size);
-                for (int d = 0; d < DB; ++d)
-                  tma_load_3d(dst + d * kBlk + (a - c0 + o) * 128, &maps.bar[kv][c.level], fullb, d * 64, hk, src + o);
+          if (kind == 0) {  // a lane per (document, box, block of 64 elements)
+            constexpr int kPer = 2 * DB;
+            for (int r0 = doc0; r0 < p.k && first_key[r0] < c0 + rows; r0 += 32 / kPer) {
+              const int r = r0 + lane / kPer, i = lane % kPer / DB, d = lane % DB;
+              if (r < p.k && first_key[r] < c0 + rows) {
+                const int a = max(first_key[r], c0), run = min(first_key[r + 1], c0 + rows) - a;
+                const Cover c = cover_doc(run);
+                if (i < c.count) {
+                  const int o = i ? run - c.size : 0;
+                  tma_load_3d(dst + d * kBlk + (a - c0 + o) * 128, &maps.bar[kv][c.level], fullb, d * 64, hk,
+                              first_row[r] + (a - first_key[r]) + o);
+                }
               }
             }
+          } else if (kv == 0) {
+            if (lane < DB)
+              tma_load_4d(dst + lane * kBlk, kind == 1 ? &maps.k_loc : &maps.k_draft, fullb, lane * 64, hk,
+                          kind == 1 ? j0 : d0, b);
           } else if (kind == 1) {
-            const bool whole = rows == kTile;
-            const Cover c = cover_of(rows);
-            const int count = whole ? 1 : c.count;
-            if (lane < count * DB) {
-              const int i = lane / DB, d = lane % DB, o = whole ? 0 : min(i * c.size, rows - c.size);
-              tma_load_4d(dst + d * kBlk + o * 128, &maps.loc[kv][whole ? 3 : c.level], fullb, d * 64, hk, j0 + o, b);
+            const Cover c = cover_tail(rows);
+            if (lane < c.count * DB) {
+              const int i = lane / DB, d = lane % DB, o = min(i * c.size, rows - c.size);
+              tma_load_4d(dst + d * kBlk + o * 128, &maps.v_loc[c.level], fullb, d * 64, hk, j0 + o, b);
             }
           } else {
-            for (int d = 0; d < DB; ++d) {
-              uint8_t* to = dst + d * kBlk + lane * 1024;
-              if (bits == 0xFFu)
-                tma_load_4d(to, &maps.draft[kv][1], fullb, d * 64, hk, d0 + 8 * lane, b);
-              else
-                for (int r = 0; r < 8; ++r)
-                  if (bits >> r & 1) tma_load_4d(to + r * 128, &maps.draft[kv][0], fullb, d * 64, hk, d0 + 8 * lane + r, b);
+            const bool whole = bits == 0xFFu;
+            if (whole)
+              for (int d = 0; d < DB; ++d)
+                tma_load_4d(dst + d * kBlk + lane * 1024, &maps.v_draft[1], fullb, d * 64, hk, d0 + 8 * lane, b);
+            if (__any_sync(0xffffffffu, bits != 0 && !whole)) {  // groups of 8 with holes, or the last one: row by row
+              for (int r = 0; r < 8; ++r)
+                if (!whole && (bits >> r & 1))
+                  for (int d = 0; d < DB; ++d)
+                    tma_load_4d(dst + d * kBlk + lane * 1024 + r * 128, &maps.v_draft[0], fullb, d * 64, hk,
+                                d0 + 8 * lane + r, b);
             }
           }
           __syncwarp();
@@ -645,6 +656,18 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         if (++st == p.ring) {
           st = 0;
           ph ^= 1;
+        }
+        if (t == lo && lane == 0 && (p.by_item ? lo == 0 : first && lo > 0)) {
+          // the note for the merge: of a cut item by the CTA that begins it (per item), or by the
+          // first CTA that it reaches (per CTA)
+          const long long w0 = w - lo;  // tile w is in the CTA floor(((w + 1) N - 1) / W)
+          const int ca = p.by_item ? (int)blockIdx.x : divide((w0 + 1) * n_act - 1, total);
+          const int cz = divide((w0 + T) * n_act - 1, total);
+          const size_t at = p.by_item ? (size_t)(b * p.n_rb + rb) * p.n_kv + hk : (size_t)blockIdx.x;
+          if (p.by_item || ca + 1 == (int)blockIdx.x) {
+            p.merges[2 * at + 1] = make_int4(ca, cz, 2 * ca + (begin_of(ca) == w0 ? 0 : 1), 0);
+            p.merges[2 * at] = make_int4(ca == cz ? -1 : b, t0, hk, n);
+          }
         }
       }
       w += hi - lo;
@@ -915,6 +938,10 @@ template <int D, int NT, int kAhead>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeP p) {
   constexpr int kRows = 1024 / D;
   pdl_enter();
+  if (p.by_item) {  // an item without drafts in use has no tiles and no note
+    const int rb = blockIdx.y / p.n_kv % p.n_rb;
+    if (rb * NT * p.TT >= drafts_of(p, blockIdx.y / p.n_kv / p.n_rb)) return;
+  }
   const int4 it = p.merges[2 * blockIdx.y], cs = p.merges[2 * blockIdx.y + 1];
   const int b = it.x, n = it.w, c0 = cs.x, c1 = cs.y;
   if (b < 0) return;
@@ -1004,9 +1031,10 @@ cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   constexpr int kRows = 1024 / D;
   const int row_groups = NT == 1 ? (p.M * p.G + kRows - 1) / kRows : NT * 128 / kRows;
   // many items: about two parts each, and many threads; few items: many parts, their loads in flight
-  // together (1m case: 18 parts, 16 ahead; 16m case: 2 parts, 18 us with 8 ahead and 9 us with 4)
-  auto merge = (int64_t)p.B * p.n_rb * p.n_kv * 4 > n_ctas ? tree_combine_kernel<D, NT, 2> : tree_combine_kernel<D, NT, 16>;
-  return launch_pdl(merge, dim3(row_groups, n_ctas), dim3(256), 0, s, p);
+  // together
+  const int n_items = p.B * p.n_rb * p.n_kv;
+  auto merge = n_items * 4 > n_ctas ? tree_combine_kernel<D, NT, 2> : tree_combine_kernel<D, NT, 16>;
+  return launch_pdl(merge, dim3(row_groups, p.by_item ? n_items : n_ctas), dim3(256), 0, s, p);
 }
 
 struct TreeWs {
@@ -1066,6 +1094,7 @@ msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaSt
   p.topk_idx = c.topk_idx;
   p.out = static_cast<__nv_bfloat16*>(c.out);
   p.merges = w.merges;
+  p.by_item = (int64_t)c.B * sh.n_rb * d.n_kv <= sm_count();
   p.sel = w.sel;
   p.part_o = w.part_o;
   p.part_ml = w.part_ml;
@@ -1101,13 +1130,13 @@ msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaSt
                                   CU_TENSOR_MAP_SWIZZLE_128B);
   };
   msa_status st = map4(&maps.q, c.q, d.n_q, c.M, qrow, p.G, p.TT);
-  const void* src[3][2] = {{c.K_bar, c.V_bar}, {c.K_loc, c.V_loc}, {c.K_draft, c.V_draft}};
-  for (int kv = 0; kv < 2; ++kv) {
-    for (int i = 0; i < 3 && c.k > 0 && st == MSA_OK; ++i) st = map3(&maps.bar[kv][i], src[0][kv], kBoxRows[i]);
-    for (int i = 0; i < 4 && c.t_loc_max > 0 && st == MSA_OK; ++i)
-      st = map4(&maps.loc[kv][i], src[1][kv], d.n_kv, c.t_loc_max, row, 1, kBoxRows[i]);
-    for (int i = 0; i < 2 && st == MSA_OK; ++i) st = map4(&maps.draft[kv][i], src[2][kv], d.n_kv, c.M, row, 1, kBoxRows[i]);
+  for (int i = 0; i < 14 && c.k > 0 && st == MSA_OK; ++i) st = map3(&maps.bar[i / 7][i % 7], i < 7 ? c.K_bar : c.V_bar, 1 << i % 7);
+  if (c.t_loc_max > 0) {
+    if (st == MSA_OK) st = map4(&maps.k_loc, c.K_loc, d.n_kv, c.t_loc_max, row, 1, kTile);
+    for (int i = 0; i < 4 && st == MSA_OK; ++i) st = map4(&maps.v_loc[i], c.V_loc, d.n_kv, c.t_loc_max, row, 1, kTailRows[i]);
   }
+  if (st == MSA_OK) st = map4(&maps.k_draft, c.K_draft, d.n_kv, c.M, row, 1, kTile);
+  for (int i = 0; i < 2 && st == MSA_OK; ++i) st = map4(&maps.v_draft[i], c.V_draft, d.n_kv, c.M, row, 1, kTailRows[i]);
   if (st != MSA_OK) return st;
   if (c.k > 0 && c.B > kSmallB) {
     TraceScope ts(kKTreePlan, s);
