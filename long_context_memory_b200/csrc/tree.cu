@@ -236,9 +236,11 @@ __device__ __forceinline__ float row_max(uint32_t addr, const uint32_t (&see)[4]
 }
 
 // The scores again, a quarter at a time with the next one's load in flight: weights 2^(s c + neg) as
-// bf16 pairs over the columns of quarters already read; returns their fp32 sum.
+// bf16 pairs to columns `to` .. (their own place, or those of quarters already read); returns their
+// fp32 sum.
 template <bool MASKED>
-__device__ __forceinline__ float row_weights(uint32_t addr, const uint32_t (&see)[4], float c, float neg) {
+__device__ __forceinline__ float row_weights(uint32_t addr, uint32_t to, const uint32_t (&see)[4], float c, float neg,
+                                             uint64_t* read_bar) {
   float sa[32], sb[32];
   const uint64_t c2 = pack_f32x2(c, c), neg2 = pack_f32x2(neg, neg);
   uint64_t sum[2] = {0, 0};  // two pairs of fp32 zeros
@@ -248,6 +250,11 @@ __device__ __forceinline__ float row_weights(uint32_t addr, const uint32_t (&see
     float(&cur)[32] = q & 1 ? sb : sa;
     tmem_ld_wait_for(cur);
     if (q < 3) tmem_ld32(addr + 32 * (q + 1), q & 1 ? sa : sb);
+    if (q == 3 && read_bar) {  // the scores are read: their place is free
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(read_bar);
+    }
     if (MASKED) hide(cur, see[q]);
     uint32_t u[16];
 #pragma unroll
@@ -257,7 +264,7 @@ __device__ __forceinline__ float row_weights(uint32_t addr, const uint32_t (&see
       sum[e & 1] = add_f32x2(sum[e & 1], pack_f32x2(a, z));
       u[e] = pack_bf16x2(a, z);
     }
-    tmem_st16(addr + 16 * q, u);
+    tmem_st16(to + 16 * q, u);
   }
   const float2 both = unpack_f32x2(add_f32x2(sum[0], sum[1]));
   return both.x + both.y;
@@ -315,11 +322,15 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
   constexpr int kTB = DB * kBlk;        // bytes of a tile
   constexpr int kThreads = 320;
   constexpr int kSoftWarps = 8;
+  // Tensor memory: scores of stream s at 128 s, its output at 256 + 128 s.  A head of 64 leaves room
+  // behind the output for the weights, so that the next scores need not wait until the products with
+  // the weights are done; a head of 128 has the weights over the scores.
+  constexpr bool kApart = D == 64;
   // (declared with the alignment that is sure behind the statically sized part; a stricter one would
   // be taken on trust and fold the rounding below away)
   extern __shared__ __align__(16) uint8_t sm_raw[];
   __shared__ uint64_t kfull[kMaxRing], kempty[kMaxRing], vfull[kMaxRing], vempty[kMaxRing];
-  __shared__ uint64_t qfull, qempty, sfull[2], pready[2], pvdone[2], ofree[2], joined, taken, hfull[2], hempty[2], drained;
+  __shared__ uint64_t qfull, qempty, sfull[2], sfree[2], pready[2], pvdone[2], ofree[2], joined, taken, hfull[2], hempty[2], drained;
   __shared__ float2 state[NT == 1 ? kTile : 1];  // one row tile: stream 1's reference maximum and sum of each row
   __shared__ int hdr[2][kHWords];
   __shared__ int q_sel[kSmallB], q_loc[kSmallB], q_n[kSmallB];  // small batches: pooled rows, local rows, drafts
@@ -353,6 +364,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
     mbar_init(&taken, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
+      mbar_init(&sfree[i], 4);
       mbar_init(&pready[i], 4);
       mbar_init(&pvdone[i], 1);
       mbar_init(&ofree[i], 4);
@@ -682,7 +694,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
     // =======================================================================
     // MMA issuer
     // =======================================================================
-    if (lane == 0) {
+    {
       constexpr uint32_t idesc_s = umma_idesc_bf16(128, 128);
       constexpr uint32_t idesc_o = umma_idesc_bf16(128, D) | kIdescBMnMajor;
       const uint64_t qd = umma_desc_k_sw128(smem_u32(qs)), kd = umma_desc_k_sw128(smem_u32(ks)),
@@ -692,18 +704,21 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
       uint32_t x = 0;
       bool ok = true;
       auto scores = [&](int i, uint32_t xx) {  // S of row tile i and key tile xx
-        if (i == 0 && !mbar_wait_short(&kfull[ks_st], ks_ph, &abort_flag)) return false;
+        if (i == 0 && !warp_wait_short(&kfull[ks_st], ks_ph, &abort_flag)) return false;
         tc_fence_after();
         const uint32_t slot = NT == 1 ? (xx & 1) : i;
         const uint64_t a = qd + (uint64_t)(i * kTB / 16), k = kd + (uint64_t)(ks_st * (kTB / 16));
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < D / 16; ++s) {
-          const int o = ((s >> 2) * kBlk + (s & 3) * 32) / 16;
-          umma_bf16(tmem + slot * 128, a + o, k + o, idesc_s, s > 0);
+          for (int s = 0; s < D / 16; ++s) {
+            const int o = ((s >> 2) * kBlk + (s & 3) * 32) / 16;
+            umma_bf16(tmem + slot * 128, a + o, k + o, idesc_s, s > 0);
+          }
+          umma_commit(&sfull[slot]);
+          if (i == NT - 1) umma_commit(&kempty[ks_st]);
         }
-        umma_commit(&sfull[slot]);
+        __syncwarp();
         if (i == NT - 1) {
-          umma_commit(&kempty[ks_st]);
           if (++ks_st == p.ring) {
             ks_st = 0;
             ks_ph ^= 1;
@@ -713,16 +728,20 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
       };
       auto weigh = [&](int i, uint32_t xx, bool first) {  // O += P V
         const uint32_t slot = NT == 1 ? (xx & 1) : i;
-        if (i == 0 && !mbar_wait_short(&vfull[vs_st], vs_ph, &abort_flag)) return false;
-        if (!mbar_wait_short(&pready[slot], (NT == 1 ? xx >> 1 : xx) & 1, &abort_flag)) return false;
+        if (i == 0 && !warp_wait_short(&vfull[vs_st], vs_ph, &abort_flag)) return false;
+        if (!warp_wait_short(&pready[slot], (NT == 1 ? xx >> 1 : xx) & 1, &abort_flag)) return false;
         tc_fence_after();
         const uint64_t v = vd + (uint64_t)(vs_st * (kTB / 16));
+        if (elect_one()) {
 #pragma unroll
-        for (int s = 0; s < kTile / 16; ++s)
-          umma_bf16_ts(tmem + 256 + slot * 128, tmem + slot * 128 + s * 8, v + s * (2048 / 16), idesc_o, !first || s > 0);
-        umma_commit(&pvdone[slot]);
+          for (int s = 0; s < kTile / 16; ++s)
+            umma_bf16_ts(tmem + 256 + slot * 128, tmem + (kApart ? 320 : 0) + slot * 128 + s * 8, v + s * (2048 / 16),
+                         idesc_o, !first || s > 0);
+          umma_commit(&pvdone[slot]);
+          if (i == NT - 1) umma_commit(&vempty[vs_st]);
+        }
+        __syncwarp();
         if (i == NT - 1) {
-          umma_commit(&vempty[vs_st]);
           if (++vs_st == p.ring) {
             vs_st = 0;
             vs_ph ^= 1;
@@ -732,24 +751,36 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
       };
       for (int j = 0; ok; ++j) {
         const int hb = j & 1;
-        if (!mbar_wait_short(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
+        if (!warp_wait_short(&hfull[hb], (j >> 1) & 1, &abort_flag)) break;
         if (hdr[hb][kHb] < 0) break;
         const int T = hdr[hb][kHhi] - hdr[hb][kHlo];
-        mbar_arrive(&hempty[hb]);
-        if (!mbar_wait_short(&qfull, j & 1, &abort_flag)) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&hempty[hb]);
+        if (!warp_wait_short(&qfull, j & 1, &abort_flag)) break;
         tc_fence_after();
+        // The scores are one step of their stream ahead of the weights: with two row tiles those of the
+        // next key tile, with one those of the next key tile but one.
+        constexpr int kAhead = NT == 1 ? 2 : 1;
         for (int i = 0; i < NT && ok; ++i) ok = scores(i, x);
+        if (NT == 1 && ok && T > 1) ok = scores(0, x + 1);
+        if (T <= kAhead && elect_one()) umma_commit(&qempty);  // every product with these queries is issued
         for (int t = 0; t < T && ok; ++t, ++x) {
-          if (NT == 1 && t + 1 < T) ok = scores(0, x + 1);
-          if (t + 1 == T) umma_commit(&qempty);  // every product with these queries is issued
           for (int i = 0; i < NT && ok; ++i) {
-            if (t == 0 && j > 0) ok = mbar_wait_short(&ofree[i], (j - 1) & 1, &abort_flag);
-            if (ok) ok = weigh(i, x, NT == 1 ? t < 2 : t == 0);  // the stream's first tile of the item
-            if (NT == 2 && ok && t + 1 < T) ok = scores(i, x + 1);
+            const uint32_t slot = NT == 1 ? (x & 1) : i;
+            const bool more = t + kAhead < T;
+            if (kApart && more) {
+              ok = warp_wait_short(&sfree[slot], (NT == 1 ? x >> 1 : x) & 1, &abort_flag);
+              if (ok) ok = scores(i, x + kAhead);
+            }
+            if (ok && t == 0 && j > 0) ok = warp_wait_short(&ofree[i], (j - 1) & 1, &abort_flag);
+            if (ok) ok = weigh(i, x, t < kAhead);  // the stream's first tile of the item
+            if (!kApart && ok && more) ok = scores(i, x + kAhead);
           }
+          if (t + kAhead + 1 == T && elect_one()) umma_commit(&qempty);
         }
       }
-      if (abort_flag) {  // what was issued ends before the tensor memory is freed
+      __syncwarp();
+      if (abort_flag && elect_one()) {  // what was issued ends before the tensor memory is freed
         umma_commit(&drained);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(&drained, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
@@ -834,14 +865,18 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         }
         if (grow) m_ref = m_new;
         const float neg = m_ref == -INFINITY ? 0.f : -m_ref;
-        l += all ? row_weights<false>(s_addr, see, p.scale_log2, neg) : row_weights<true>(s_addr, see, p.scale_log2, neg);
-        tmem_st_wait();
-        // the products of the tile before have ended when those of this one may start: one phase of
-        // pvdone is outstanding at a time
-        if (t > t_first && !any && !warp_wait_short(&pvdone[str], (n - 1) & 1, &abort_flag)) {
+        // Weights apart from the scores: the products with the ones before have to be done.  Over the
+        // scores: sfull came after them.  (Either way one phase of pvdone is outstanding at a time.)
+        if (kApart && t > t_first && !any && !warp_wait_short(&pvdone[str], (n - 1) & 1, &abort_flag)) {
           ok = false;
           break;
         }
+        if (kApart) tc_fence_after();
+        const uint32_t p_addr = kApart ? o_addr + 64 : s_addr;
+        uint64_t* read_bar = kApart ? &sfree[str] : nullptr;
+        l += all ? row_weights<false>(s_addr, p_addr, see, p.scale_log2, neg, read_bar)
+                 : row_weights<true>(s_addr, p_addr, see, p.scale_log2, neg, read_bar);
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&pready[str]);
