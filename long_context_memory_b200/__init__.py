@@ -1,7 +1,8 @@
 """Memory Sparse Attention (MSA) hot path for NVIDIA B200: Python binding.
 
-A thin ctypes layer over ``libmsa.so`` (C ABI declared in ``include/msa.h``).
-It only marshals arguments: every step of the path runs in the library's CUDA
+A thin ctypes layer over ``libmsa.so`` (C ABI declared in ``include/msa.h``); the calls that a decode
+step makes by the dozen (rotation, norms, draft trees) go through ``_fastcall``, the same marshalling
+compiled against PyTorch's headers.  It only marshals arguments: every step of the path runs in the library's CUDA
 kernels.  PyTorch supplies device memory (outputs and workspaces) and the
 current stream.  The library is loaded on the first call into it, and that
 call raises ImportError when the library is missing; there is no CPU fallback.
@@ -16,7 +17,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 from typing import Optional
 
 __all__ = [
@@ -83,10 +83,6 @@ class Rotary(ctypes.Structure):
                 ("high", ctypes.c_double), ("magnitude", ctypes.c_double)]
 
 
-# msa_heads: in, out, in_row, in_head, out_row, out_head, heads, reserved
-_HEADS = struct.Struct("@PPqqqqii")
-
-
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -95,7 +91,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     P, I32, I64, SZ, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
     DP = ctypes.POINTER(Dims)
-    RP = HP = P  # msa_rotary by address, msa_heads as packed bytes (_heads)
+    RP, HP = ctypes.POINTER(Rotary), P
     sig = {
         "msa_last_error": (ctypes.c_char_p, []),
         "msa_version": (I32, []),
@@ -133,8 +129,8 @@ def _load():
         "msa_head_norm_rotate_grad": (I32, [RP, I32, HP, HP, HP, HP, I64, P, P, F, F, P, P, P, P, SZ, P]),
         "msa_tree_plan": (I32, [P, P, P, I32, I32, I32, P, P, P]),
         "msa_tree_attend_workspace_size": (SZ, [DP, I32, I32, I32, I32]),
-        "msa_tree_attend": (I32, [P, P, P, P, P, P, I32, I32, P, P, P, I32, P, P, P, I32, I32, P, I32, F, P, P, SZ, P]),
-        "msa_tree_commit": (I32, [P, P, P, P, P, I32, I32, I32, P, P, P, I32, P, P]),
+        "msa_tree_attend": (I32, [DP, P, P, P, P, P, I32, I32, P, P, P, I32, P, P, P, I32, I32, P, I32, F, P, P, SZ, P]),
+        "msa_tree_commit": (I32, [DP, P, P, P, P, I32, I32, I32, P, P, P, I32, P, P]),
         "msa_trace_enable": (I32, [I32]),
         "msa_trace_reset": (I32, []),
         "msa_trace_num_kernels": (I32, []),
@@ -549,7 +545,6 @@ def attend_merge(o_shares, lse2_shares, out=None, stream=None):
 # ----------------------------------------------------------------------------
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "yarn": 4}
-_DTYPES: dict = {}  # torch dtype -> msa_dtype (filled on first use)
 
 
 def rotary(head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", base: float = 1e6,
@@ -575,81 +570,35 @@ def rotary_turns(rot: Rotary):
     import numpy as np
 
     out = np.zeros(max(1, rot.rot_dim // 2), dtype=np.uint64)
-    _check(lib.msa_rotary_turns(ctypes.addressof(rot), out.ctypes.data))
+    _check(lib.msa_rotary_turns(ctypes.byref(rot), out.ctypes.data))
     return out
 
 
-def _bind_torch() -> None:
-    """Fill the module's torch names (the module imports without torch)."""
-    global _torch, _cur_device, _raw_stream
+_torch = None
+_fast = None
+
+
+def _load_fast():
+    """The checks of the calls below (_fastcall, beside the library): loaded on the first of them."""
+    global _torch, _fast
+    import importlib.util
+
     import torch
 
-    _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
-    _cur_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
-    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    _torch = torch
-
-
-_torch = None
-_cur_device = _raw_stream = None
-
-
-def _on_device(t, name: str) -> int:
-    """The index of t's CUDA device, which must be the current one (the library launches there)."""
-    if _torch is None:
-        _bind_torch()
-    dev = t.get_device()
-    if dev < 0 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor, got {t.device}")
-    if dev != _cur_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{_cur_device()}")
-    return dev
-
-
-def _dtype_code(dtype, name: str) -> int:
-    code = _DTYPES.get(dtype)
-    if code is None:
-        raise ValueError(f"{name}: dtype must be bfloat16, float16 or float32, got {dtype}")
-    return code
-
-
-def _flat(t, name: str, shape, dtype, dev: int) -> int:
-    """The address of t, which must be a contiguous tensor of this shape and dtype on device dev."""
-    if t.shape != shape or t.dtype != dtype or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}")
-    return t.data_ptr()
-
-
-def _heads(x, out, name: str, rows: int, head_dim: int, dtype, dev: int) -> bytes:
-    """msa_heads of x [rows, heads, head_dim], its output in ``out`` (None: no output) of the same
-    shape; both with any strides but contiguous head elements."""
-    sx = x.stride()
-    if x.dim() != 3 or x.dtype != dtype or x.get_device() != dev or sx[2] != 1:
-        raise ValueError(f"{name}: expected [rows, heads, {head_dim}] {dtype} on cuda:{dev} with contiguous head "
-                         f"elements, got {tuple(x.shape)} {x.dtype} on {x.device}, strides {sx}")
-    sh = x.shape
-    if sh[0] != rows or sh[2] != head_dim or sh[1] < 1:
-        raise ValueError(f"{name}: expected [{rows}, heads, {head_dim}], got {tuple(sh)}")
-    if out is None:
-        return _HEADS.pack(x.data_ptr(), 0, sx[0], sx[1], 0, 0, sh[1], 0)
-    so = out.stride()
-    if out.shape != sh or out.dtype != dtype or out.get_device() != dev or so[2] != 1:
-        raise ValueError(f"the output of {name}: expected {tuple(sh)} {dtype} on cuda:{dev} with contiguous head "
-                         f"elements, got {tuple(out.shape)} {out.dtype} on {out.device}, strides {so}")
-    return _HEADS.pack(x.data_ptr(), out.data_ptr(), sx[0], sx[1], so[0], so[1], sh[1], 0)
-
-
-def _launch_stream(stream, dev: int):
-    if stream is None and _raw_stream is not None:
-        return _raw_stream(dev)
-    return _stream(stream)
+    lib.msa_version()  # the library itself: ImportError when it is missing
+    path = os.path.join(_HERE, "_fastcall.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_fastcall.so not found at {path}; build it with `python -m long_context_memory_b200.build`")
+    spec = importlib.util.spec_from_file_location("_fastcall", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    mod.bind(LIB_PATH)
+    _torch, _fast = torch, mod
+    return mod
 
 
 def _used_on(stream, *tensors) -> None:
     """Tell the allocator that tensors allocated here are used on the caller's ``stream``."""
-    if stream is None or not tensors:
-        return
     st = _torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
     if st != _torch.cuda.current_stream():
         for t in tensors:
@@ -657,17 +606,12 @@ def _used_on(stream, *tensors) -> None:
                 t.record_stream(st)
 
 
-def _norm_weight(w, name: str, rot: Rotary, dtype, dev: int):
-    return None if w is None else _flat(w, name, (rot.head_dim,), dtype, dev)
+def _handle(stream):
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
-def _rows_of(rot, q, positions):
-    """(device, dtype, rows, address of the positions) of a call on heads q."""
-    dev = _on_device(q, "q")
-    rows = q.shape[0] if q.dim() == 3 else -1
-    if rows < 0:
-        raise ValueError(f"q: expected [rows, heads, {rot.head_dim}], got {tuple(q.shape)}")
-    return dev, q.dtype, rows, _flat(positions, "positions", (rows,), _torch.int32, dev)
+def _like(t):
+    return _torch.empty_like(t, memory_format=_torch.contiguous_format)
 
 
 def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_out=None, stream=None):
@@ -676,24 +620,22 @@ def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_ou
     bf16, fp16 or fp32; rows and heads may be strided (slices of a fused projection).  ``out`` /
     ``k_out`` may be q / k themselves (in place).  ``grad`` applies the transposed rotation: the
     gradient of the call, given the gradient of its output.  Returns out, or (out, k_out) with k."""
-    dev, dt, rows, pos = _rows_of(rot, q, positions)
-    code, D = _dtype_code(dt, "q"), rot.head_dim
+    fast = _fast or _load_fast()
     new = ()
     if out is None:
-        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        out = _like(q)
         new = (out,)
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
-        hk = None
-    else:
-        if k_out is None:
-            k_out = _torch.empty_like(k, memory_format=_torch.contiguous_format)
-            new += (k_out,)
-        hk = _heads(k, k_out, "k", rows, D, dt, dev)
-    _check(lib.msa_rotate(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, rows, pos,
-                          1 if grad else 0, _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+    elif k_out is None:
+        k_out = _like(k)
+        new += (k_out,)
+    st = fast.rotate(rot, q, positions, k, grad, out, k_out, _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
 
@@ -702,25 +644,22 @@ def head_norm_rotate(rot: Rotary, q, k, q_weight, k_weight, positions, eps: floa
     """RMS norm of every query and key head, times (weight_offset + weight), then the rotation, in
     one pass.  q, k [rows, heads, head_dim] as for ``rotate`` (k may be None); weights [head_dim] of
     the same dtype, or None.  Returns (out, k_out), or out without k."""
-    dev, dt, rows, pos = _rows_of(rot, q, positions)
-    code, D = _dtype_code(dt, "q"), rot.head_dim
-    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
+    fast = _fast or _load_fast()
     new = ()
     if out is None:
-        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        out = _like(q)
         new = (out,)
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
-        hk = None
-    else:
-        if k_out is None:
-            k_out = _torch.empty_like(k, memory_format=_torch.contiguous_format)
-            new += (k_out,)
-        hk = _heads(k, k_out, "k", rows, D, dt, dev)
-    _check(lib.msa_head_norm_rotate(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, rows, wq, wk,
-                                    weight_offset, eps, pos, _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+    elif k_out is None:
+        k_out = _like(k)
+        new += (k_out,)
+    st = fast.head_norm_rotate(rot, q, k, q_weight, k_weight, positions, eps, weight_offset, out, k_out, _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
 
@@ -730,29 +669,22 @@ def head_norm_append(rot: Rotary, q, k, v, q_weight, k_weight, positions, slots,
     (normalised, rotated) and the values to row ``slots[r]`` of their query's local cache
     K_loc, V_loc [B, t_loc_max, n_kv, head_dim] (rows / B rows per query, in order).  A slot of -1
     leaves the row out of the cache.  Returns out."""
-    dev, dt, rows, pos = _rows_of(rot, q, positions)
-    code, D = _dtype_code(dt, "q"), rot.head_dim
-    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
+    fast = _fast or _load_fast()
     new = ()
     if out is None:
-        out = _torch.empty_like(q, memory_format=_torch.contiguous_format)
+        out = _like(q)
         new = (out,)
-    hk, hv = _heads(k, None, "k", rows, D, dt, dev), _heads(v, None, "v", rows, D, dt, dev)
-    if K_loc.dim() != 4 or v.shape != k.shape:
-        raise ValueError(f"expected K_loc [B, t_loc_max, n_kv, head_dim] and v of k's shape, got {tuple(K_loc.shape)}, "
-                         f"{tuple(v.shape)}, {tuple(k.shape)}")
-    B, t_loc_max = K_loc.shape[0], K_loc.shape[1]
-    cache = (B, t_loc_max, k.shape[1], D)
-    _check(lib.msa_head_norm_append(ctypes.addressof(rot), code, _heads(q, out, "q", rows, D, dt, dev), hk, hv, rows, wq,
-                                    wk, weight_offset, eps, pos, _flat(slots, "slots", (rows,), _torch.int32, dev),
-                                    _flat(K_loc, "K_loc", cache, dt, dev), _flat(V_loc, "V_loc", cache, dt, dev), B,
-                                    t_loc_max, _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+    st = fast.head_norm_append(rot, q, k, v, q_weight, k_weight, positions, slots, K_loc, V_loc, eps, weight_offset, out,
+                               _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out
 
 
 def head_norm_grad_workspace_size(rot: Rotary, rows: int, n_q: int, n_k: int) -> int:
-    return int(lib.msa_head_norm_grad_workspace_size(ctypes.addressof(rot), rows, n_q, n_k))
+    return int(lib.msa_head_norm_grad_workspace_size(ctypes.byref(rot), rows, n_q, n_k))
 
 
 def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, dk, eps: float = 1e-6,
@@ -761,37 +693,22 @@ def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, 
 
     Returns (gradient of q, of k, of q_weight [head_dim] fp32, of k_weight fp32); ``out`` takes the
     four tensors.  k and dk may be None together (the second and fourth are then None)."""
-    if (k is None) != (dk is None):
-        raise ValueError("k and dk go together")
-    dev, dt, rows, pos = _rows_of(rot, q, positions)
-    code, D = _dtype_code(dt, "q"), rot.head_dim
-    wq, wk = _norm_weight(q_weight, "q_weight", rot, dt, dev), _norm_weight(k_weight, "k_weight", rot, dt, dev)
-    hq = _heads(q, None, "q", rows, D, dt, dev)
-    hk = None if k is None else _heads(k, None, "k", rows, D, dt, dev)
-    f32, new = _torch.float32, []
+    fast = _fast or _load_fast()
+    new = []
     if out is None:
-        gq = _torch.empty_like(q, memory_format=_torch.contiguous_format)
-        gk = None if k is None else _torch.empty_like(k, memory_format=_torch.contiguous_format)
-        gwq = _torch.empty(D, dtype=f32, device=q.device)
-        gwk = None if k is None else _torch.empty(D, dtype=f32, device=q.device)
-        new = [gq, gk, gwq, gwk]
-    else:
-        gq, gk, gwq, gwk = out
-    if dq.shape != q.shape or (k is not None and dk.shape != k.shape):
-        raise ValueError("dq and dk must have the shapes of q and k")
-    hdq = _heads(dq, gq, "dq", rows, D, dt, dev)
-    hdk = None if k is None else _heads(dk, gk, "dk", rows, D, dt, dev)
-    awq = None if gwq is None else _flat(gwq, "out[2]", (D,), f32, dev)
-    awk = None if gwk is None else _flat(gwk, "out[3]", (D,), f32, dev)
+        out = (_like(q), None if k is None else _like(k), _torch.empty(rot.head_dim, dtype=_torch.float32, device=q.device),
+               None if k is None else _torch.empty(rot.head_dim, dtype=_torch.float32, device=q.device))
+        new = list(out)
     if ws is None:
-        nbytes = head_norm_grad_workspace_size(rot, rows, q.shape[1], 0 if k is None else k.shape[1])
-        ws = _workspace(nbytes, q.device)
+        ws = _workspace(head_norm_grad_workspace_size(rot, q.shape[0], q.shape[-2], 0 if k is None else k.shape[-2]), q.device)
         new.append(ws)
-    else:  # the library checks the caller's buffer against what it needs
-        nbytes = max(0, ws.numel() * ws.element_size() - 256)
-    _check(lib.msa_head_norm_rotate_grad(ctypes.addressof(rot), code, hq, hk, hdq, hdk, rows, wq, wk, weight_offset, eps,
-                                         pos, awq, awk, _aligned_ptr(ws), nbytes, _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+    gq, gk, gwq, gwk = out
+    st = fast.head_norm_rotate_grad(rot, q, k, q_weight, k_weight, positions, dq, dk, eps, weight_offset, gq, gk, gwq, gwk,
+                                    ws, _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return gq, gk, gwq, gwk
 
 
@@ -803,22 +720,17 @@ def tree_plan(parents, loc_len, pos_offset: int, n_draft=None, out=None, stream=
 
     ``parents`` [B, M] int32: an earlier draft, or -1 for one that follows the committed context of
     ``loc_len`` [B] tokens; ``n_draft`` [B] int32: drafts in use (None: all)."""
-    dev = _on_device(parents, "parents")
-    if parents.dim() != 2:
-        raise ValueError(f"parents: expected [B, M], got {tuple(parents.shape)}")
-    i32 = _torch.int32
-    shape = parents.shape
-    B, M = shape
-    words = (B, M, (M + 31) // 32)
+    fast = _fast or _load_fast()
     new = ()
     if out is None:
-        out = new = (_torch.empty(words, dtype=i32, device=parents.device), _torch.empty_like(parents, dtype=i32))
-    _check(lib.msa_tree_plan(_flat(parents, "parents", shape, i32, dev),
-                             None if n_draft is None else _flat(n_draft, "n_draft", (B,), i32, dev),
-                             _flat(loc_len, "loc_len", (B,), i32, dev), B, M, pos_offset,
-                             _flat(out[0], "out[0]", words, i32, dev), _flat(out[1], "out[1]", shape, i32, dev),
-                             _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+        B, M = parents.shape
+        out = new = (_torch.empty((B, M, (M + 31) // 32), dtype=_torch.int32, device=parents.device),
+                     _torch.empty((B, M), dtype=_torch.int32, device=parents.device))
+    st = fast.tree_plan(parents, loc_len, pos_offset, n_draft, out[0], out[1], _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out
 
 
@@ -836,53 +748,21 @@ def tree_attend(dims, q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft=
     ``tree_plan``'s positions).  ``mask`` [B, M, ceil(M/32)] int32 from ``tree_plan``.  The memory
     arguments (as for ``sparse_attend``) go together; without them the drafts attend over cache and
     drafts alone.  A draft t >= n_draft[b] and a row that sees no key give zeros."""
-    dd = Dims.of(dims)
-    dev = _on_device(q, "q")
-    if q.dim() != 4:
-        raise ValueError(f"q: expected [B, M, n_q, head_dim], got {tuple(q.shape)}")
-    B, M = q.shape[0], q.shape[1]
-    bf, i32 = _torch.bfloat16, _torch.int32
-    n_kv, D = dd.n_kv, dd.head_dim
-    rows = (B, M, dd.n_q, D)
-    drafts = (B, M, n_kv, D)
-    if (K_loc is None) != (V_loc is None):
-        raise ValueError("K_loc and V_loc go together")
-    t_loc_max, kl, vl = 0, None, None
-    if K_loc is not None:
-        t_loc_max = K_loc.shape[1] if K_loc.dim() == 4 else -1
-        cache = (B, t_loc_max, n_kv, D)
-        kl, vl = _flat(K_loc, "K_loc", cache, bf, dev), _flat(V_loc, "V_loc", cache, bf, dev)
-        if t_loc_max == 0:
-            kl = vl = None
-    k = n_docs = n_chunks = 0
-    kb = vb = co = top = None
-    if K_bar is not None or V_bar is not None or chunk_off is not None or topk_idx is not None:
-        if K_bar is None or V_bar is None or chunk_off is None or topk_idx is None:
-            raise ValueError("K_bar, V_bar, chunk_off and topk_idx go together")
-        k, n_docs, n_chunks = topk_idx.shape[-1], chunk_off.numel() - 1, K_bar.shape[0]
-        memory = (n_chunks, n_kv, D)
-        kb, vb = _flat(K_bar, "K_bar", memory, bf, dev), _flat(V_bar, "V_bar", memory, bf, dev)
-        co, top = _flat(chunk_off, "chunk_off", (n_docs + 1,), i32, dev), _flat(topk_idx, "topk_idx", (B, k), i32, dev)
-        if k == 0:
-            kb = vb = co = top = None
-    new = []
+    fast = _fast or _load_fast()
+    new = ()
     if out is None:
-        out = _torch.empty_like(q)
-        new.append(out)
-    if ws is not None:  # the library checks the caller's buffer against what it needs
-        nbytes = max(0, ws.numel() * ws.element_size() - 256)
-    else:
-        nbytes = tree_attend_workspace_size(dims, B, M, k, t_loc_max)
-        ws = _workspace(nbytes, q.device)
-        new.append(ws)
-    _check(lib.msa_tree_attend(ctypes.addressof(dd), _flat(q, "q", rows, bf, dev),
-                               _flat(K_draft, "K_draft", drafts, bf, dev), _flat(V_draft, "V_draft", drafts, bf, dev),
-                               _flat(mask, "mask", (B, M, (M + 31) // 32), i32, dev),
-                               None if n_draft is None else _flat(n_draft, "n_draft", (B,), i32, dev), B, M, kl, vl,
-                               _flat(loc_len, "loc_len", (B,), i32, dev), t_loc_max, kb, vb, co, n_docs, n_chunks, top,
-                               k, softmax_scale, _flat(out, "out", rows, bf, dev), _aligned_ptr(ws), nbytes,
-                               _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+        out = _like(q)
+        new = (out,)
+    if ws is None:
+        ws = _workspace(max(1, tree_attend_workspace_size(dims, q.shape[0], q.shape[1], 0 if topk_idx is None else topk_idx.shape[-1],
+                                                          0 if K_loc is None else K_loc.shape[1])), q.device)
+        new += (ws,)
+    st = fast.tree_attend(Dims.of(dims), q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft, K_bar, V_bar, chunk_off,
+                          topk_idx, softmax_scale, out, ws, _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out
 
 
@@ -890,34 +770,17 @@ def tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out=None,
     """Append the accepted drafts to the local caches: row path[b, i] of K_draft / V_draft
     [B, M, n_kv, head_dim] to slot loc_len[b] + i of K_loc / V_loc, for i < n_path[b].  Returns the
     new lengths [B] int32 (``out``, which must not be ``loc_len``)."""
-    dev = _on_device(K_draft, "K_draft")
-    if K_draft.dim() != 4 or K_loc.dim() != 4 or path.dim() != 2:
-        raise ValueError("expected K_draft [B, M, n_kv, head_dim], K_loc [B, t_loc_max, n_kv, head_dim], path [B, A]")
-    drafts = K_draft.shape
-    B, M, n_kv, D = drafts
-    t_loc_max, A = K_loc.shape[1], path.shape[1]
-    cache, one = (B, t_loc_max, n_kv, D), (B,)
-    bf, i32 = _torch.bfloat16, _torch.int32
+    fast = _fast or _load_fast()
     new = ()
     if out is None:
-        out = _torch.empty(B, dtype=i32, device=K_draft.device)
+        out = _torch.empty_like(loc_len)
         new = (out,)
-    _check(lib.msa_tree_commit(ctypes.addressof(_kv_dims(n_kv, D)), _flat(K_draft, "K_draft", drafts, bf, dev),
-                               _flat(V_draft, "V_draft", drafts, bf, dev), _flat(path, "path", (B, A), i32, dev),
-                               _flat(n_path, "n_path", one, i32, dev), B, M, A, _flat(K_loc, "K_loc", cache, bf, dev),
-                               _flat(V_loc, "V_loc", cache, bf, dev), _flat(loc_len, "loc_len", one, i32, dev),
-                               t_loc_max, _flat(out, "out", one, i32, dev), _launch_stream(stream, dev)))
-    _used_on(stream, *new)
+    st = fast.tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out, _handle(stream))
+    if st:
+        _check(st)
+    if new and stream is not None:
+        _used_on(stream, *new)
     return out
-
-
-def _kv_dims(n_kv: int, head_dim: int) -> Dims:
-    """A dims struct of which only the KV heads matter."""
-    key = ("kv", n_kv, head_dim)
-    hit = _DIMS_CACHE.get(key)
-    if hit is None:
-        hit = _DIMS_CACHE[key] = Dims(64, n_kv, n_kv, head_dim, 1, 64, 64, 1e6)
-    return hit
 
 
 # ----------------------------------------------------------------------------

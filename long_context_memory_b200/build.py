@@ -1,4 +1,5 @@
-"""Build libmsa.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build libmsa.so (the C-ABI library) in-tree with nvcc for sm_100a, and _fastcall (the binding's checks
+of latency-bound calls) with the host compiler against PyTorch's headers."""
 from __future__ import annotations
 
 import os
@@ -11,15 +12,33 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["msa_api.cu", "route.cu", "route_static.cu", "attend.cu", "encode.cu", "aux_loss.cu", "tiered.cu",
            "rotary.cu", "tree.cu"]
 LIB = os.path.join(HERE, "libmsa.so")
+FAST = os.path.join(HERE, "_fastcall.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(FAST):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "msa.h")]
     return any(os.path.getmtime(p) > t for p in deps)
+
+
+def fastcall_command() -> list:
+    """The compiler command of _fastcall.so."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    cuda = os.path.dirname(os.path.dirname(NVCC))
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    return ([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+            + [f"-I{d}" for d in cpp_extension.include_paths() + [os.path.join(cuda, "include"),
+                                                                  sysconfig.get_paths()["include"]]]
+            + [os.path.join(CSRC, "fastcall.cpp"), "-o", FAST, f"-L{lib}", "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-lc10_cuda", "-ldl"])
 
 
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -34,6 +53,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(prefix="msa_build_") as tmp:
         objs = [os.path.join(tmp, os.path.splitext(src)[0] + ".o") for src in SOURCES]
         cmds = [flags + ["-c", os.path.join(CSRC, src), "-o", obj] for src, obj in zip(SOURCES, objs)]
+        cmds.append(fastcall_command())
         if verbose:
             for c in cmds:
                 print(" ".join(c), flush=True)
@@ -42,7 +62,7 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         for r in results:
             if r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
-                raise RuntimeError("nvcc failed building libmsa.so")
+                raise RuntimeError("compiling libmsa.so or _fastcall.so failed")
             if verbose or ptxas_verbose:
                 sys.stderr.write(r.stderr)
         link = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-rdc=true", "-shared", "-Xcompiler", "-fPIC",

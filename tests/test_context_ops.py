@@ -1,6 +1,7 @@
 """Host-side tests of the rotation, per-head norm and draft-tree calls: the frequency tables, the
 oracle's gradients against differences, and the refusals of the C ABI and the binding (no GPU)."""
 import ctypes
+import struct
 
 import numpy as np
 import pytest
@@ -58,7 +59,7 @@ def test_oracle_gradients_match_differences():
 
 def _heads(msa, heads=4, D=64, inp=FAKE, out=FAKE, in_row=None, in_head=None, out_row=None, out_head=None):
     pick = lambda v, d: d if v is None else v
-    return msa._HEADS.pack(inp or 0, out or 0, pick(in_row, heads * D), pick(in_head, D), pick(out_row, heads * D),
+    return struct.pack("@PPqqqqii", inp or 0, out or 0, pick(in_row, heads * D), pick(in_head, D), pick(out_row, heads * D),
                            pick(out_head, D), heads, 0)
 
 
@@ -216,40 +217,44 @@ def test_binding_refuses_tensors_off_the_device(msa):
         msa.rotate(msa.rotary(64), q, pos)
     with pytest.raises(ValueError, match="CUDA"):
         msa.tree_plan(torch.zeros(1, 4, dtype=torch.int32), pos[:1], 0)
+    kv, n = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32)
     with pytest.raises(ValueError, match="CUDA"):
-        msa.tree_commit(torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16), None, None, None, None, None, None)
+        msa.tree_commit(kv, kv, torch.zeros(1, 2, dtype=torch.int32), n, kv, kv, n)
+    with pytest.raises(ValueError, match="expected a tensor"):
+        msa.tree_commit(kv, None, torch.zeros(1, 2, dtype=torch.int32), n, kv, kv, n)
+    with pytest.raises(ValueError, match="structure"):
+        msa.rotate(_dims(msa), q, pos)
 
 
-def test_binding_refuses_wrong_shapes_and_types(msa, monkeypatch):
-    """The binding's checks, on host tensors with the device check stood in for."""
+def test_binding_refuses_wrong_shapes_and_types(msa):
+    """Shapes, types and strides are checked before the device: host tensors are told what was expected
+    of them (the call whose tensors fit is told that it wants CUDA tensors)."""
     import torch
 
-    msa._bind_torch()
-    monkeypatch.setattr(msa, "_on_device", lambda t, name: t.get_device())
     r = msa.rotary(64)
     q, k, pos = torch.zeros(4, 3, 64), torch.zeros(4, 2, 64), torch.zeros(4, dtype=torch.int32)
     for args, kw in [((r, q.double(), pos), {}), ((r, q[..., :32], pos), {}), ((r, q.reshape(12, 64), pos), {}),
                      ((r, q.transpose(1, 2).contiguous().transpose(1, 2), pos), {}), ((r, q, pos[:3]), {}),
                      ((r, q, pos.long()), {}), ((r, q, pos), dict(k=k[:3])), ((r, q, pos), dict(k=k.half())),
                      ((r, q, pos), dict(out=q[:3])), ((r, q, pos), dict(k_out=k)), ((r, q, pos), dict(k=k, k_out=q))]:
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
             msa.rotate(*args, **kw)
     w = torch.ones(64)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
         msa.head_norm_rotate(r, q, k, w[:32], w, pos)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
         msa.head_norm_rotate_grad(r, q, k, w, w, pos, q, None)
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
         msa.head_norm_rotate_grad(r, q, k, w, w, pos, q[:, :2], k)
     cache = torch.zeros(2, 9, 2, 64)
     for bad in (dict(v=q), dict(slots=pos[:2]), dict(K_loc=cache[:, :, :1]), dict(V_loc=cache.half()), dict(K_loc=k)):
         a = {**dict(v=k, slots=pos, K_loc=cache, V_loc=cache), **bad}
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
             msa.head_norm_append(r, q, k, a["v"], w, w, pos, a["slots"], a["K_loc"], a["V_loc"])
     par = torch.zeros(2, 40, dtype=torch.int32)
     for bad in (dict(parents=par[0]), dict(parents=par.long()), dict(loc=pos[:3]), dict(n=pos[:3])):
         a = {**dict(parents=par, loc=pos[:2], n=None), **bad}
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
             msa.tree_plan(a["parents"], a["loc"], 0, n_draft=a["n"])
     bf = torch.bfloat16
     d = _dims(msa)
@@ -259,7 +264,7 @@ def test_binding_refuses_wrong_shapes_and_types(msa, monkeypatch):
     for bad in (dict(q=t["q"][:, :, :4]), dict(q=t["q"].float()), dict(mask=t["mask"][..., :1]), dict(K_loc=None),
                 dict(loc_len=pos), dict(V_draft=t["V_draft"][:, :39]), dict(K_bar=t["K_loc"][0]),
                 dict(out=t["q"][:1]), dict(n_draft=pos), dict(V_loc=t["V_loc"][:, :8])):
-        with pytest.raises(ValueError):
+        with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
             msa.tree_attend(d, **{**t, **bad})
-    with pytest.raises(ValueError):
+    with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
         msa.tree_commit(t["K_draft"], t["V_draft"], par[:1], pos[:2], t["K_loc"], t["V_loc"], pos[:2])
