@@ -35,12 +35,8 @@ namespace msa {
 
 namespace {
 
-#ifndef ROT_CTAS
-#define ROT_CTAS 2
-#define ROT_U 2
-#define GRAD_CTAS 2
-#define GRAD_U 2
-#endif
+constexpr int kRotCtas = 2, kRotBatch = 2;    // CTAs per SM, iterations whose loads are in flight together
+constexpr int kGradCtas = 2, kGradBatch = 2;  // (the gradients')
 constexpr int kMaxPairs = 128;  // rot_dim / 2 of the largest head
 
 struct HeadsP {
@@ -272,8 +268,8 @@ __device__ __forceinline__ void row_angles(const RotP& p, const uint64_t* turns,
 // a time.  The weights are folded into the rotation's factors, which stay in registers over the heads
 // of a class: y = (x (w p) + x' (w' q)) r; two elements per instruction throughout.
 template <typename T, int V, int J, bool NORM, bool INTER>
-__global__ void __launch_bounds__(256, ROT_CTAS) rotate_kernel(const __grid_constant__ RotP p) {
-  constexpr int U = J == 1 ? ROT_U : 1;  // iterations whose loads are in flight together
+__global__ void __launch_bounds__(256, kRotCtas) rotate_kernel(const __grid_constant__ RotP p) {
+  constexpr int U = J == 1 ? kRotBatch : 1;  // iterations whose loads are in flight together
   constexpr bool PAIRED = INTER || V == 1;
   using X = Vec<T, V>;
   __shared__ uint64_t turns[kMaxPairs];
@@ -446,8 +442,8 @@ __global__ void __launch_bounds__(256, ROT_CTAS) rotate_kernel(const __grid_cons
 // registers; a CTA sums its warps in order and writes one partial per weight.
 //   z = Rot^T(dy), u = z w, n = x r:  dx = r u - (r^2 mean(u n)) x,  dw += z n
 template <typename T, int V, int J, bool INTER>
-__global__ void __launch_bounds__(256, GRAD_CTAS) norm_grad_kernel(const __grid_constant__ RotP p) {
-  constexpr int U = J == 1 ? GRAD_U : 1;
+__global__ void __launch_bounds__(256, kGradCtas) norm_grad_kernel(const __grid_constant__ RotP p) {
+  constexpr int U = J == 1 ? kGradBatch : 1;
   constexpr bool PAIRED = INTER || V == 1;
   using X = Vec<T, V>;
   extern __shared__ float red[];  // [warps][D]
@@ -623,7 +619,7 @@ bool vec_ok(const void* ptr, int64_t s0, int64_t s1, int v, int size) {
 // workspace holds one partial per CTA
 int grad_ctas(int64_t rows, int its) {
   const int64_t warps = rows * std::max(1, its);
-  return (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8, GRAD_CTAS * sm_count()));
+  return (int)std::max<int64_t>(1, std::min<int64_t>((warps + 7) / 8, kGradCtas * sm_count()));
 }
 
 template <typename T, int V, int J>
@@ -631,7 +627,7 @@ cudaError_t launch_forward(const RotP& p, bool norm, cudaStream_t s) {
   const int64_t warps = p.rows * p.parts;
   // few warps: a small CTA on each of many SMs; many: 8 warps per CTA, persistent, three CTAs per SM
   const int wpc = warps >= 8LL * sm_count() ? 8 : (int)std::max<int64_t>(1, warps / sm_count());
-  const dim3 grid((unsigned)std::min<int64_t>((warps + wpc - 1) / wpc, ROT_CTAS * sm_count()));
+  const dim3 grid((unsigned)std::min<int64_t>((warps + wpc - 1) / wpc, kRotCtas * sm_count()));
   auto kern = norm ? (p.interleaved ? rotate_kernel<T, V, J, true, true> : rotate_kernel<T, V, J, true, false>)
                    : (p.interleaved ? rotate_kernel<T, V, J, false, true> : rotate_kernel<T, V, J, false, false>);
   return launch_pdl(kern, grid, dim3(32 * wpc), 0, s, p);
@@ -768,8 +764,11 @@ msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall&
     p.its += h.its;
     p.classes = i + 1;
   }
-  // shares of a row: enough warps for every SM when there are few rows
-  const int64_t want = 16LL * sm_count();
+  // Shares of a row: every SM's warps when there are few rows, and, for the forward kernels, several
+  // rounds of the persistent warps (a round that is half empty costs the share of a round that it
+  // leaves idle: 8193 rows of 40 heads in fp32, 3.5 rounds, 68 us whole and 63 us in two shares; the
+  // gradients lose more on the second angle table of a row than that, 61 against 67 us)
+  const int64_t want = (c.mode == 2 ? 16LL : 96LL) * sm_count();
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.its, (want + p.rows - 1) / std::max<int64_t>(1, p.rows)));
   int ctas = 0;
   if (c.mode == 2) {

@@ -407,13 +407,18 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         rows[u] = -1;
         if (i < pairs) {
           const int doc = p.topk_idx[i];
-          if (doc >= 0 && doc < p.n_docs) rows[u] = doc_rows(p, doc);
+          const bool known = doc >= 0 && doc < p.n_docs;
+          if (known) rows[u] = doc_rows(p, doc);
           else raise_dev_error(kDevErrBadIndex);
+          if (p.B == 1) {  // the only query's table
+            tab[i] = max(rows[u], 0);
+            tab[p.k + 1 + i] = known ? p.chunk_off[doc] : 0;
+          }
         }
       }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        if (rows[u] > 0) atomicAdd(&q_sel[(i0 + u * 64) / p.k], rows[u]);
+        if (rows[u] > 0) atomicAdd(&q_sel[p.B == 1 ? 0 : (i0 + u * 64) / p.k], rows[u]);
     }
   }
   __syncthreads();
@@ -427,37 +432,50 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
     query(b, sel, L, n);
     return (long long)p.n_kv * blocks_of<NT>(p, n) * tiles_of(sel, L, n);
   };
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += cost_of(b);
-  long long incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  long long base = incl - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) base += warp_sum[w];
-    total += warp_sum[w];
-  }
   // CTA c of the n_act with work begins at tile floor(c total / n_act)
-  const int n_act = (int)max(1ll, min((long long)gridDim.x, total));
+  long long total = 0, w_begin = 0, w_end = 0;
+  int n_act = 1;
   auto begin_of = [&](int c) { return min(total, muldiv(total, c, n_act)); };
-  const long long w_begin = begin_of(blockIdx.x), w_end = begin_of(blockIdx.x + 1);
-  for (int b = b0; b < b1 && w_begin < w_end; ++b) {
-    const long long c = cost_of(b);
-    if (base <= w_begin && w_begin < base + c) {
-      first_b = b;
-      first_base = base;
+  auto cut = [&] {
+    n_act = (int)max(1ll, min((long long)gridDim.x, total));
+    w_begin = begin_of(blockIdx.x);
+    w_end = begin_of(blockIdx.x + 1);
+  };
+  if (p.B == 1) {  // (only the producer needs it)
+    if (warp == kSoftWarps) {
+      total = cost_of(0);
+      cut();
     }
-    base += c;
+  } else {
+    const int per = (p.B + kThreads - 1) / kThreads;
+    const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += cost_of(b);
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long base = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) base += warp_sum[w];
+      total += warp_sum[w];
+    }
+    cut();
+    for (int b = b0; b < b1 && w_begin < w_end; ++b) {
+      const long long c = cost_of(b);
+      if (base <= w_begin && w_begin < base + c) {
+        first_b = b;
+        first_base = base;
+      }
+      base += c;
+    }
+    __syncthreads();
   }
-  __syncthreads();
 
   if (warp == kSoftWarps) {
     // =======================================================================
@@ -468,8 +486,8 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
     int n_items = 0;
     bool ok = true;
     long long w = w_begin;
-    long long bbase = first_base;
-    int b = first_b;
+    long long bbase = p.B == 1 ? 0 : first_base;
+    int b = p.B == 1 ? 0 : first_b;
     bool fresh = true, listed = false;  // b is new; its documents are in the table
     int L = 0, n = 0, sel = 0, T = 0;
     int *first_key = tab, *first_row = tab + p.k + 1;
@@ -547,7 +565,9 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
             __syncwarp();
             for (int q = 0; q < each; ++q) {
               const int r = lane * each + q;
-              if (r < p.k) {
+              if (r < p.k && p.B == 1) {
+                sum += first_key[r];
+              } else if (r < p.k) {
                 const int doc = p.topk_idx[(size_t)b * p.k + r];
                 int n_rows = 0, row0 = 0;
                 if (doc >= 0 && doc < p.n_docs) {
