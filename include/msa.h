@@ -628,7 +628,8 @@ msa_status msa_head_norm_rotate(const msa_rotary* rot, msa_dtype dtype, const ms
  * K_loc, V_loc [B, t_loc_max, k->heads, head_dim] of the call's dtype, contiguous;
  * k->out and v->out are unused.  slots [rows] device int32: -1 leaves the row out
  * of the cache (a padded row); another slot outside [0, t_loc_max) is left out too
- * and raises device error bit 1.  Two rows of a query must not share a slot. */
+ * and raises device error bit 1.  Two rows of a query must not share a slot.  The caches
+ * overlap neither each other nor the call's other tensors. */
 msa_status msa_head_norm_append(const msa_rotary* rot, msa_dtype dtype, const msa_heads* q, const msa_heads* k,
                                 const msa_heads* v, int64_t rows, const void* q_weight, const void* k_weight,
                                 float weight_offset, float eps, const int32_t* positions, const int32_t* slots,
@@ -668,6 +669,7 @@ msa_status msa_head_norm_rotate_grad(const msa_rotary* rot, msa_dtype dtype, con
  *              is set where draft j is t or an ancestor of t; rows t >= n_draft are 0.
  *   positions  [B, M] device int32 out: pos_offset + loc_len + depth, depth = the number
  *              of ancestors (0 for rows t >= n_draft).
+ * mask and positions overlap no input.
  * Limits: 1 <= B <= 65535, 1 <= M <= 256, pos_offset >= 0.
  * ------------------------------------------------------------------------- */
 msa_status msa_tree_plan(const int32_t* parents, const int32_t* n_draft, const int32_t* loc_len, int32_t B, int32_t M,
@@ -689,11 +691,12 @@ msa_status msa_tree_plan(const int32_t* parents, const int32_t* n_draft, const i
  *   out        [B, M, n_q, head_dim] bf16.  A row that sees no key is 0.
  * Keys and values outside loc_len and n_draft, and of drafts that no row of the query
  * sees, may hold anything (NaN and infinities included).  A value row that some row of
- * its query sees must be finite.
+ * its query sees must be finite, or that query's rows are undefined (other queries' are not
+ * touched).  out overlaps no input.
  * Rounding: products of bf16 with fp32 accumulation; softmax statistics fp32; the
  * weights of the values are rounded to bf16 for the tensor cores.
  * Limits: head_dim in {64, 128}; n_kv <= 8; n_q / n_kv <= 16; 1 <= M <= 256;
- * 1 <= B <= 4096; k <= min(n_docs, 256).
+ * 1 <= B <= 4096; k <= min(n_docs, 256); k * n_chunks < 2^31.
  */
 size_t msa_tree_attend_workspace_size(const msa_dims* dims, int32_t B, int32_t M, int32_t k, int32_t t_loc_max);
 msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_draft, const void* V_draft,
@@ -709,7 +712,7 @@ msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_dr
  * A draft at depth i was rotated at the position its row gets here, so no key is
  * turned again.  path [B, A] device int32, ids in [0, M); an id or a slot outside its
  * range is left out and raises device error bit 1.  new_len [B] device int32 out must
- * not be loc_len itself.  Rows behind the last appended one are left as they were.
+ * not be loc_len itself; drafts and caches do not overlap.  Rows behind the last appended one are left as they were.
  * Limits: 1 <= A <= M <= 256; 1 <= B <= 65535. */
 msa_status msa_tree_commit(const msa_dims* dims, const void* K_draft, const void* V_draft, const int32_t* path,
                            const int32_t* n_path, int32_t B, int32_t M, int32_t A, void* K_loc, void* V_loc,

@@ -597,13 +597,21 @@ def _load_fast():
     return mod
 
 
-def _used_on(stream, *tensors) -> None:
-    """Tell the allocator that tensors allocated here are used on the caller's ``stream``."""
+def _made(stream, make):
+    """The tensors of ``make()``, allocated for use on ``stream``: memory that the current stream has
+    given back may still be in use by its pending work, which ``stream`` does not wait for."""
+    if stream is None:
+        return make()
     st = _torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
-    if st != _torch.cuda.current_stream():
-        for t in tensors:
-            if t is not None:
-                t.record_stream(st)
+    cur = _torch.cuda.current_stream()
+    if st == cur:
+        return make()
+    with _torch.cuda.stream(st):
+        made = make()
+    for t in made if isinstance(made, tuple) else (made,):
+        if t is not None:
+            t.record_stream(cur)  # the caller's stream uses it next
+    return made
 
 
 def _handle(stream):
@@ -621,21 +629,16 @@ def rotate(rot: Rotary, q, positions, k=None, grad: bool = False, out=None, k_ou
     ``k_out`` may be q / k themselves (in place).  ``grad`` applies the transposed rotation: the
     gradient of the call, given the gradient of its output.  Returns out, or (out, k_out) with k."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
-        out = _like(q)
-        new = (out,)
+        out = _like(q) if stream is None else _made(stream, lambda: _like(q))
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
     elif k_out is None:
-        k_out = _like(k)
-        new += (k_out,)
+        k_out = _like(k) if stream is None else _made(stream, lambda: _like(k))
     st = fast.rotate(rot, q, positions, k, grad, out, k_out, _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
 
@@ -645,21 +648,16 @@ def head_norm_rotate(rot: Rotary, q, k, q_weight, k_weight, positions, eps: floa
     one pass.  q, k [rows, heads, head_dim] as for ``rotate`` (k may be None); weights [head_dim] of
     the same dtype, or None.  Returns (out, k_out), or out without k."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
-        out = _like(q)
-        new = (out,)
+        out = _like(q) if stream is None else _made(stream, lambda: _like(q))
     if k is None:
         if k_out is not None:
             raise ValueError("k_out without k")
     elif k_out is None:
-        k_out = _like(k)
-        new += (k_out,)
+        k_out = _like(k) if stream is None else _made(stream, lambda: _like(k))
     st = fast.head_norm_rotate(rot, q, k, q_weight, k_weight, positions, eps, weight_offset, out, k_out, _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out if k is None else (out, k_out)
 
 
@@ -670,16 +668,12 @@ def head_norm_append(rot: Rotary, q, k, v, q_weight, k_weight, positions, slots,
     K_loc, V_loc [B, t_loc_max, n_kv, head_dim] (rows / B rows per query, in order).  A slot of -1
     leaves the row out of the cache.  Returns out."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
-        out = _like(q)
-        new = (out,)
+        out = _like(q) if stream is None else _made(stream, lambda: _like(q))
     st = fast.head_norm_append(rot, q, k, v, q_weight, k_weight, positions, slots, K_loc, V_loc, eps, weight_offset, out,
                                _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out
 
 
@@ -694,21 +688,17 @@ def head_norm_rotate_grad(rot: Rotary, q, k, q_weight, k_weight, positions, dq, 
     Returns (gradient of q, of k, of q_weight [head_dim] fp32, of k_weight fp32); ``out`` takes the
     four tensors.  k and dk may be None together (the second and fourth are then None)."""
     fast = _fast or _load_fast()
-    new = []
     if out is None:
-        out = (_like(q), None if k is None else _like(k), _torch.empty(rot.head_dim, dtype=_torch.float32, device=q.device),
-               None if k is None else _torch.empty(rot.head_dim, dtype=_torch.float32, device=q.device))
-        new = list(out)
+        weight = lambda: _torch.empty(rot.head_dim, dtype=_torch.float32, device=q.device)
+        out = _made(stream, lambda: (_like(q), None if k is None else _like(k), weight(), None if k is None else weight()))
     if ws is None:
-        ws = _workspace(head_norm_grad_workspace_size(rot, q.shape[0], q.shape[-2], 0 if k is None else k.shape[-2]), q.device)
-        new.append(ws)
+        size = head_norm_grad_workspace_size(rot, q.shape[0], q.shape[-2], 0 if k is None else k.shape[-2])
+        ws = _made(stream, lambda: _workspace(size, q.device))
     gq, gk, gwq, gwk = out
     st = fast.head_norm_rotate_grad(rot, q, k, q_weight, k_weight, positions, dq, dk, eps, weight_offset, gq, gk, gwq, gwk,
                                     ws, _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return gq, gk, gwq, gwk
 
 
@@ -721,16 +711,13 @@ def tree_plan(parents, loc_len, pos_offset: int, n_draft=None, out=None, stream=
     ``parents`` [B, M] int32: an earlier draft, or -1 for one that follows the committed context of
     ``loc_len`` [B] tokens; ``n_draft`` [B] int32: drafts in use (None: all)."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
         B, M = parents.shape
-        out = new = (_torch.empty((B, M, (M + 31) // 32), dtype=_torch.int32, device=parents.device),
-                     _torch.empty((B, M), dtype=_torch.int32, device=parents.device))
+        out = _made(stream, lambda: (_torch.empty((B, M, (M + 31) // 32), dtype=_torch.int32, device=parents.device),
+                                     _torch.empty((B, M), dtype=_torch.int32, device=parents.device)))
     st = fast.tree_plan(parents, loc_len, pos_offset, n_draft, out[0], out[1], _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out
 
 
@@ -749,20 +736,16 @@ def tree_attend(dims, q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft=
     arguments (as for ``sparse_attend``) go together; without them the drafts attend over cache and
     drafts alone.  A draft t >= n_draft[b] and a row that sees no key give zeros."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
-        out = _like(q)
-        new = (out,)
+        out = _like(q) if stream is None else _made(stream, lambda: _like(q))
     if ws is None:
-        ws = _workspace(max(1, tree_attend_workspace_size(dims, q.shape[0], q.shape[1], 0 if topk_idx is None else topk_idx.shape[-1],
-                                                          0 if K_loc is None else K_loc.shape[1])), q.device)
-        new += (ws,)
+        size = tree_attend_workspace_size(dims, q.shape[0], q.shape[1], 0 if topk_idx is None else topk_idx.shape[-1],
+                                          0 if K_loc is None else K_loc.shape[1])
+        ws = _made(stream, lambda: _workspace(max(1, size), q.device))
     st = fast.tree_attend(Dims.of(dims), q, K_draft, V_draft, mask, K_loc, V_loc, loc_len, n_draft, K_bar, V_bar, chunk_off,
                           topk_idx, softmax_scale, out, ws, _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out
 
 
@@ -771,15 +754,11 @@ def tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out=None,
     [B, M, n_kv, head_dim] to slot loc_len[b] + i of K_loc / V_loc, for i < n_path[b].  Returns the
     new lengths [B] int32 (``out``, which must not be ``loc_len``)."""
     fast = _fast or _load_fast()
-    new = ()
     if out is None:
-        out = _torch.empty_like(loc_len)
-        new = (out,)
+        out = _made(stream, lambda: _torch.empty_like(loc_len))
     st = fast.tree_commit(K_draft, V_draft, path, n_path, K_loc, V_loc, loc_len, out, _handle(stream))
     if st:
         _check(st)
-    if new and stream is not None:
-        _used_on(stream, *new)
     return out
 
 

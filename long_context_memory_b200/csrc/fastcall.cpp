@@ -238,6 +238,7 @@ PyObject* py_head_norm_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // a workspace tensor: its 256-byte aligned address and the bytes from there
 void workspace(PyObject* o, void** ws, size_t* bytes) {
   const at::Tensor& t = tensor(o, "ws");
+  if (!t.is_contiguous()) refuse("ws: expected a contiguous tensor, got strides %s", text(t.strides()).c_str());
   const size_t p = reinterpret_cast<size_t>(t.data_ptr()), at = (p + 255) & ~size_t(255);
   const size_t have = t.nbytes();
   *ws = reinterpret_cast<void*>(at);

@@ -912,6 +912,12 @@ static msa_status check_rotary(const msa_rotary* r, msa_dtype dtype) {
 
 static bool misaligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
 
+// do two ranges of bytes share one
+static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 // one msa_heads argument: its input, and its output where the call writes one
 static msa_status check_heads(const msa_heads* h, const char* name, const msa_rotary* r, msa_dtype dtype, int64_t rows,
                               bool needs_in, bool needs_out) {
@@ -1028,6 +1034,8 @@ msa_status msa_head_norm_append(const msa_rotary* rot, msa_dtype dtype, const ms
     if (!slots || misaligned(slots, 4)) return fail(MSA_ERR_INVALID_ARG, "slots is NULL or not 4-byte aligned");
     if (!K_loc || !V_loc || misaligned(K_loc, size) || misaligned(V_loc, size))
       return fail(MSA_ERR_INVALID_ARG, "K_loc or V_loc is NULL or not aligned to its type");
+    const size_t cache = (size_t)B * t_loc_max * k->heads * rot->head_dim * size;
+    if (overlap(K_loc, cache, V_loc, cache)) return fail(MSA_ERR_INVALID_ARG, "K_loc and V_loc overlap");
   }
   if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
   if (rows == 0) return MSA_OK;
@@ -1116,6 +1124,13 @@ msa_status msa_tree_plan(const int32_t* parents, const int32_t* n_draft, const i
   CHECK_PTR(loc_len);
   CHECK_PTR(mask);
   CHECK_PTR(positions);
+  const size_t rows = (size_t)B * M * 4, words = rows * ((M + 31) / 32), per_query = (size_t)B * 4;
+  for (const void* in : {static_cast<const void*>(parents), static_cast<const void*>(n_draft), static_cast<const void*>(loc_len)}) {
+    const size_t n = in == parents ? rows : per_query;
+    if (overlap(in, n, mask, words) || overlap(in, n, positions, rows))
+      return fail(MSA_ERR_INVALID_ARG, "mask and positions must not overlap the inputs");
+  }
+  if (overlap(mask, words, positions, rows)) return fail(MSA_ERR_INVALID_ARG, "mask and positions overlap");
   if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
   return tree_plan_launch(parents, n_draft, loc_len, B, M, pos_offset, mask, positions, static_cast<cudaStream_t>(stream));
 }
@@ -1156,11 +1171,18 @@ msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_dr
     if (n_docs < 1 || n_chunks < n_docs)
       return fail(MSA_ERR_INVALID_ARG, "need 1 <= n_docs <= n_chunks (got %d, %d)", n_docs, n_chunks);
     if (k > n_docs) return fail(MSA_ERR_INVALID_ARG, "k must be <= n_docs (got %d, %d)", k, n_docs);
+    if ((int64_t)k * n_chunks > (int64_t)INT32_MAX)
+      return fail(MSA_ERR_INVALID_ARG, "k * n_chunks must be below 2^31 (got %d * %d)", k, n_chunks);
     CHECK_PTR(K_bar);
     CHECK_PTR(V_bar);
     CHECK_PTR(chunk_off);
     CHECK_PTR(topk_idx);
   }
+  const size_t row = (size_t)dims->n_kv * dims->head_dim * 2, rows = (size_t)B * M * dims->n_q * dims->head_dim * 2;
+  if (overlap(out, rows, q, rows) || overlap(out, rows, K_draft, B * M * row) || overlap(out, rows, V_draft, B * M * row) ||
+      (t_loc_max > 0 && (overlap(out, rows, K_loc, (size_t)B * t_loc_max * row) || overlap(out, rows, V_loc, (size_t)B * t_loc_max * row))) ||
+      (k > 0 && (overlap(out, rows, K_bar, n_chunks * row) || overlap(out, rows, V_bar, n_chunks * row))))
+    return fail(MSA_ERR_INVALID_ARG, "out must not overlap the inputs");
   const size_t need = tree_attend_workspace(*dims, B, M, k, t_loc_max);
   if (ws_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);
   if (need && (!ws || misaligned(ws, 256)))
@@ -1187,7 +1209,14 @@ msa_status msa_tree_commit(const msa_dims* dims, const void* K_draft, const void
   CHECK_PTR(V_loc);
   CHECK_PTR(loc_len);
   CHECK_PTR(new_len);
-  if (new_len == loc_len) return fail(MSA_ERR_INVALID_ARG, "new_len must not be loc_len");
+  if (overlap(new_len, (size_t)B * 4, loc_len, (size_t)B * 4) || overlap(new_len, (size_t)B * 4, n_path, (size_t)B * 4) ||
+      overlap(new_len, (size_t)B * 4, path, (size_t)B * A * 4))
+    return fail(MSA_ERR_INVALID_ARG, "new_len must not be loc_len, nor overlap the path");
+  const size_t row = (size_t)dims->n_kv * dims->head_dim * 2, drafts = B * M * row, cache = (size_t)B * t_loc_max * row;
+  if (overlap(K_loc, cache, V_loc, cache)) return fail(MSA_ERR_INVALID_ARG, "K_loc and V_loc overlap");
+  if (overlap(K_draft, drafts, K_loc, cache) || overlap(K_draft, drafts, V_loc, cache) ||
+      overlap(V_draft, drafts, K_loc, cache) || overlap(V_draft, drafts, V_loc, cache))
+    return fail(MSA_ERR_INVALID_ARG, "the drafts overlap the caches");
   if (fault_injected()) return fail(MSA_ERR_CUDA, "injected fault (MSA_FAULT=launch)");
   return tree_commit_launch(*dims, K_draft, V_draft, path, n_path, B, M, A, K_loc, V_loc, loc_len, t_loc_max, new_len,
                             static_cast<cudaStream_t>(stream));

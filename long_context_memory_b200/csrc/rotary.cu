@@ -625,7 +625,7 @@ int grad_ctas(int64_t rows, int its) {
 template <typename T, int V, int J>
 cudaError_t launch_forward(const RotP& p, bool norm, cudaStream_t s) {
   const int64_t warps = p.rows * p.parts;
-  // few warps: a small CTA on each of many SMs; many: 8 warps per CTA, persistent, three CTAs per SM
+  // few warps: a small CTA on each of many SMs; many: 8 warps per CTA, persistent, kRotCtas CTAs per SM
   const int wpc = warps >= 8LL * sm_count() ? 8 : (int)std::max<int64_t>(1, warps / sm_count());
   const dim3 grid((unsigned)std::min<int64_t>((warps + wpc - 1) / wpc, kRotCtas * sm_count()));
   auto kern = norm ? (p.interleaved ? rotate_kernel<T, V, J, true, true> : rotate_kernel<T, V, J, true, false>)

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // power of two that is not longer, the second one moved back to end with the run (the rows where
 // they overlap arrive twice, the same bytes); a box may start at any row of the tile, since the
 // 128-byte swizzle goes by the address.  Values are copied only where some draft sees them, into a
-// ring that starts as zeros: whatever stands in the rows behind a sequence, and in drafts that
+// ring whose other rows are zeros: whatever stands in the rows behind a sequence, and in drafts that
 // nobody sees, never reaches a product.  (A key too many does no harm: its score is replaced.)
 //
 // Warps: 2 x 4 softmax warps (a stream each, a thread per row), one producer (item headers, document tables, TMA),
@@ -556,6 +556,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         const int kind = t < Tc ? 0 : t < Tc + Tl ? 1 : 2;  // pooled rows, local rows, drafts
         int rows, k_rows;   // rows of the tile; rows that its key and value boxes bring
         int v_rows;
+        uint32_t keep[4];   // rows of the tile that its value boxes bring (uniform over the warp)
         int doc0 = 0;       // kind 0: the first document with keys in the tile
         uint32_t bits = 0;  // kind 2, lane < 16: drafts d0 + 8 lane .. that some draft of the query sees
         if (kind == 0) {
@@ -636,6 +637,15 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           }
           k_rows = kTile;
           v_rows = rows;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) keep[q] = seen[q];
+        }
+        if (kind != 2) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int left = rows - 32 * q;
+            keep[q] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
+          }
         }
         for (int kv = 0; kv < 2; ++kv) {
           uint64_t* fullb = (kv ? vfull : kfull) + st;
@@ -643,6 +653,21 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           if (x >= (uint32_t)p.ring && !warp_wait_short((kv ? vempty : kempty) + st, ph, &abort_flag)) {
             ok = false;
             break;
+          }
+          // The rows that no box brings still hold an older tile's, maybe of a query whose values are
+          // not finite: zeros (a slot's first tile finds the ring cleared).
+          if (kv && x >= (uint32_t)p.ring && (keep[0] & keep[1] & keep[2] & keep[3]) != ~0u) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (keep[q] == ~0u) continue;
+#pragma unroll 1
+              for (int r = lane >> 3; r < 32; r += 4)  // eight lanes a row of 128 bytes
+                if (!(keep[q] >> r & 1))
+                  for (int d = 0; d < DB; ++d)
+                    *reinterpret_cast<uint4*>(dst + d * kBlk + (q * 32 + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
           if (lane == 0) mbar_arrive_expect_tx(fullb, (kv ? v_rows : k_rows) * D * 2);
           __syncwarp();

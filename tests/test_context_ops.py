@@ -9,6 +9,7 @@ import pytest
 import context_oracle as O
 
 FAKE = 0x10000  # 16-byte aligned non-null "device" address; never dereferenced
+FAR = 0x10000000000  # far behind it: tensors that must not overlap
 
 
 @pytest.fixture(scope="module")
@@ -114,7 +115,7 @@ def test_rotate_validation(msa, no_launch):
 
 
 def _norm(msa, form, eps=1e-6, off=0.0, qw=FAKE, kw=FAKE, rows=4, ws=FAKE * 16, ws_bytes=1 << 24, B=2, T=8, slots=FAKE,
-          K=FAKE, v=None, k="k", dk="k", dkw=FAKE):
+          K=FAKE, V=FAR, v=None, k="k", dk="k", dkw=FAKE):
     r, q = msa.rotary(64), _heads(msa)
     kk = _heads(msa, 2) if k else None
     L = msa.lib
@@ -122,7 +123,7 @@ def _norm(msa, form, eps=1e-6, off=0.0, qw=FAKE, kw=FAKE, rows=4, ws=FAKE * 16, 
         return L.msa_head_norm_rotate(ctypes.byref(r), 0, q, kk, rows, qw, kw, off, eps, FAKE, None)
     if form == "append":
         return L.msa_head_norm_append(ctypes.byref(r), 0, q, kk, v or _heads(msa, 2), rows, qw, kw, off, eps, FAKE,
-                                      slots, K, FAKE, B, T, None)
+                                      slots, K, V, B, T, None)
     return L.msa_head_norm_rotate_grad(ctypes.byref(r), 0, q, kk, q, _heads(msa, 2) if dk else None, rows, qw, kw, off,
                                        eps, FAKE, FAKE, dkw, ws, ws_bytes, None)
 
@@ -145,6 +146,8 @@ def test_head_norm_append_and_grad_validation(msa, no_launch):
     assert _norm(msa, "append", T=0) == 1
     assert _norm(msa, "append", slots=None) == 1
     assert _norm(msa, "append", K=None) == 1
+    cache = 2 * 8 * 2 * 64 * 2
+    assert _norm(msa, "append", V=FAKE + cache - 16) == 1 and _norm(msa, "append", V=FAKE + cache) == 4
     assert _norm(msa, "append", v=_heads(msa, 3)) == 1  # as many value heads as key heads
     assert _norm(msa, "append", k=None) == 1
     assert _norm(msa, "backward", ws_bytes=16) == 3
@@ -162,7 +165,7 @@ def _dims(msa, **kw):
     return msa.Dims(*d.values())
 
 
-def _plan(msa, B=2, M=5, off=0, parents=FAKE, n=None, loc=FAKE, mask=FAKE, pos=FAKE):
+def _plan(msa, B=2, M=5, off=0, parents=FAKE, n=None, loc=FAKE, mask=FAR, pos=2 * FAR):
     return msa.lib.msa_tree_plan(parents, n, loc, B, M, off, mask, pos, None)
 
 
@@ -170,16 +173,17 @@ def test_tree_plan_validation(msa, no_launch):
     assert _plan(msa) == 4
     assert _plan(msa, M=256) == 4
     for bad in (dict(B=0), dict(B=65536), dict(M=0), dict(M=257), dict(off=-1), dict(parents=None), dict(loc=None),
-                dict(mask=None), dict(pos=None), dict(mask=FAKE + 4), dict(n=FAKE + 8)):
+                dict(mask=None), dict(pos=None), dict(mask=FAR + 4), dict(n=FAKE + 8),
+                dict(mask=FAKE), dict(pos=FAKE + 16), dict(pos=FAR), dict(n=3 * FAR, mask=3 * FAR)):
         assert _plan(msa, **bad) == 1, bad
 
 
 def _attend(msa, dims=None, B=2, M=5, T=10, k=0, n_docs=4, n_chunks=9, scale=0.0, ws_bytes=None, q=FAKE, K=FAKE, mem=FAKE,
-            mask=FAKE, loc=FAKE):
+            mask=FAKE, loc=FAKE, out=FAR):
     d = dims or _dims(msa)
     need = msa.lib.msa_tree_attend_workspace_size(ctypes.byref(d), B, M, k, T)
     return msa.lib.msa_tree_attend(ctypes.byref(d), q, FAKE, FAKE, mask, None, B, M, K, K, loc, T, mem, mem, mem, n_docs,
-                                   n_chunks, mem, k, scale, FAKE, FAKE * 16, need if ws_bytes is None else ws_bytes, None)
+                                   n_chunks, mem, k, scale, out, FAKE * 16, need if ws_bytes is None else ws_bytes, None)
 
 
 def test_tree_attend_validation(msa, no_launch):
@@ -187,10 +191,13 @@ def test_tree_attend_validation(msa, no_launch):
     assert _attend(msa, k=3) == 4
     assert _attend(msa, T=0, K=None) == 4              # drafts alone
     assert _attend(msa, mem=None) == 4
+    assert _attend(msa, out=FAR, q=FAR + 2 * 5 * 8 * 64 * 2) == 4
+    assert _attend(msa, k=256, n_docs=300, n_chunks=(1 << 23) - 1) == 4
     for bad in (dict(B=0), dict(B=4097), dict(M=0), dict(M=257), dict(T=-1), dict(k=-1), dict(k=257, n_docs=300, n_chunks=400),
                 dict(k=5), dict(k=3, n_chunks=3), dict(k=3, mem=None), dict(K=None), dict(q=None), dict(q=FAKE + 8),
                 dict(mask=None), dict(loc=None), dict(scale=-1.0), dict(scale=float("nan")),
-                dict(dims=_dims(msa, n_q=7))):
+                dict(dims=_dims(msa, n_q=7)), dict(out=FAKE), dict(out=FAKE + 16), dict(out=FAR, K=FAR), dict(out=FAR, k=3, mem=FAR),
+                dict(out=FAR, q=FAR + 2 * 5 * 8 * 64 * 2 - 16), dict(k=256, n_docs=300, n_chunks=1 << 23)):
         assert _attend(msa, **{**dict(ws_bytes=1 << 30), **bad}) == 1, bad
     for bad in (dict(head_dim=96), dict(n_q=34), dict(n_q=16, n_kv=16), dict(chunk=32)):
         assert _attend(msa, dims=_dims(msa, **bad), ws_bytes=1 << 30) == 2, bad
@@ -198,15 +205,18 @@ def test_tree_attend_validation(msa, no_launch):
     assert msa.lib.msa_tree_attend_workspace_size(ctypes.byref(_dims(msa, head_dim=96)), 1, 1, 0, 1) == 0
 
 
-def _commit(msa, B=2, M=5, A=3, T=9, path=FAKE, new=2 * FAKE, K=FAKE):
-    return msa.lib.msa_tree_commit(ctypes.byref(_dims(msa)), FAKE, FAKE, path, FAKE, B, M, A, K, FAKE, FAKE, T, new, None)
+def _commit(msa, B=2, M=5, A=3, T=9, path=FAKE, new=2 * FAR, K=FAR, V=3 * FAR, Kd=FAKE):
+    return msa.lib.msa_tree_commit(ctypes.byref(_dims(msa)), Kd, FAKE, path, FAKE, B, M, A, K, V, FAKE, T, new, None)
 
 
 def test_tree_commit_validation(msa, no_launch):
     assert _commit(msa) == 4
+    cache, drafts = 2 * 9 * 2 * 64 * 2, 2 * 5 * 2 * 64 * 2
     for bad in (dict(B=0), dict(M=257), dict(A=0), dict(A=6), dict(T=0), dict(path=None), dict(new=None), dict(new=FAKE),
-                dict(K=FAKE + 2)):
+                dict(K=FAR + 2), dict(V=FAR), dict(V=FAR + cache - 16), dict(Kd=FAR), dict(Kd=FAR - drafts + 16), dict(K=FAKE),
+                dict(path=2 * FAR)):
         assert _commit(msa, **bad) == 1, bad
+    assert _commit(msa, Kd=FAR - drafts) == 4 and _commit(msa, V=FAR + cache) == 4
 
 
 def test_binding_refuses_tensors_off_the_device(msa):
@@ -268,3 +278,5 @@ def test_binding_refuses_wrong_shapes_and_types(msa):
             msa.tree_attend(d, **{**t, **bad})
     with pytest.raises(ValueError, match="expected [^C]|k_out without k"):
         msa.tree_commit(t["K_draft"], t["V_draft"], par[:1], pos[:2], t["K_loc"], t["V_loc"], pos[:2])
+    with pytest.raises(ValueError, match="ws: expected a contiguous tensor"):  # one byte, however long it looks
+        msa.tree_attend(d, **t, ws=torch.zeros(1, dtype=torch.uint8).expand(1 << 24))

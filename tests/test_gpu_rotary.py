@@ -287,6 +287,26 @@ def test_layouts_of_memory_agree(msa, cuda_device):
     assert torch.equal(msa.rotate(rot, b, pos), msa.rotate(rot, b.contiguous(), pos))
 
 
+def test_rows_past_2_31_elements(msa, cuda_device):
+    import torch
+
+    gen = torch.Generator(device=cuda_device).manual_seed(2)
+    step = 1_100_000_000
+    big = torch.empty(2 * step + 256, dtype=torch.bfloat16, device=cuda_device)
+    x = big.as_strided((3, 4, 64), (step, 64, 1))
+    x.copy_(torch.randn(3, 4, 64, generator=gen, device=cuda_device))
+    small, rot = x.contiguous(), msa.rotary(64)
+    pos = torch.tensor([1, -2, 2 ** 31 - 1], dtype=torch.int32, device=cuda_device)
+    w = small[0, 0].contiguous()
+    ref = msa.head_norm_rotate(rot, small, small, w, w, pos)
+    assert all(torch.equal(a, b) for a, b in zip(msa.head_norm_rotate(rot, x, x, w, w, pos), ref))
+    ref = msa.head_norm_rotate_grad(rot, small, None, w, None, pos, small, None)
+    assert all(torch.equal(a, b) for a, b in zip(msa.head_norm_rotate_grad(rot, x, None, w, None, pos, x, None)[::2], ref[::2]))
+    ref = msa.rotate(rot, small, pos)
+    msa.rotate(rot, x, pos, out=x)  # in place
+    assert torch.equal(x, ref)
+
+
 def test_streams_and_graphs(msa, cuda_device):
     import torch
 

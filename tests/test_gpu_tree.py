@@ -224,6 +224,164 @@ def test_streams_and_graphs(msa, cuda_device):
     assert msa.check_device_errors() == 0
 
 
+def _memory(c, rng, sizes, top, dev):
+    """Documents of ``sizes`` pooled rows, ``top`` [B, k] of them for each query."""
+    import torch
+
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev).to(torch.bfloat16)
+    n_kv, D = c["Kd"].shape[2:]
+    c["off"] = np.concatenate([[0], np.cumsum(sizes)]).astype(np.int32)
+    c["top"] = np.asarray(top, dtype=np.int32)
+    c["k"] = c["top"].shape[1]
+    c["Kb"], c["Vb"] = bf(int(c["off"][-1]), n_kv, D), bf(int(c["off"][-1]), n_kv, D)
+
+
+@pytest.mark.parametrize("case", [  # B, M, n_q, n_kv, D, t_loc_max, k
+    (33, 4, 8, 2, 64, 150, 3), (70, 3, 16, 8, 128, 40, 2), (400, 2, 4, 1, 64, 20, 1), (200, 1, 8, 8, 64, 300, 0),
+    (64, 40, 8, 2, 64, 260, 0), (40, 70, 8, 4, 128, 70, 1)])
+def test_tree_attend_many_queries(msa, cuda_device, case):
+    """More queries than the kernel plans in shared memory; more items than SMs, cut at any place."""
+    import torch
+
+    B, M, n_q, n_kv, D, T, k = case
+    loc = np.random.default_rng(B).integers(0, T + 1, size=B)
+    c = _case(B, B, M, n_q, n_kv, D, T, loc, k, True, cuda_device)
+    got = _run(msa, c, cuda_device)
+    _check(got, c)
+    assert torch.equal(got, _run(msa, c, cuda_device)) and msa.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("B,M,n_q,n_kv,D", [(1, 256, 16, 1, 64), (2, 255, 32, 2, 128), (1, 9, 16, 1, 128)])
+def test_tree_attend_widest_groups(msa, cuda_device, B, M, n_q, n_kv, D):
+    c = _case(M, B, M, n_q, n_kv, D, 200, [200, 31][:B], 2, B > 1, cuda_device)
+    _check(_run(msa, c, cuda_device), c)
+
+
+@pytest.mark.parametrize("B,k,D", [(1, 256, 64), (3, 255, 128), (40, 100, 64)])
+def test_tree_attend_many_documents(msa, cuda_device, B, k, D):
+    """Empty documents, documents of one row, of exactly a tile and longer than two; the same one twice."""
+    rng = np.random.default_rng(k)
+    c = _case(k, B, 3, 4, 2, D, 20, rng.integers(0, 21, size=B), 0, True, cuda_device)
+    sizes = rng.choice([0, 1, 2, 3, 7, 31, 64, 65], size=300)
+    sizes[[3, 50, 200]] = [128, 300, 129]
+    top = np.stack([rng.permutation(300)[:k] for _ in range(B)])
+    top[:, -1] = top[:, 0]
+    top[:, :3] = [200, 50, 3]
+    _memory(c, rng, sizes, top, cuda_device)
+    _check(_run(msa, c, cuda_device), c)
+    assert msa.check_device_errors() == 0
+
+
+def test_nothing_drafted(msa, cuda_device):
+    c = _case(23, 4, 20, 8, 2, 64, 50, [50, 0, 7, 9], 1, False, cuda_device)
+    c["n_draft"][:] = 0
+    assert float(_run(msa, c, cuda_device).abs().sum()) == 0 and msa.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_query_s_values_stay_its_own(msa, cuda_device, D):
+    """Values that are not finite, in some queries' caches, documents and drafts: the others' rows do
+    not change, although their tiles take the same places."""
+    import torch
+
+    B = 64
+    rng = np.random.default_rng(D)
+    loc = rng.integers(1, 300, size=B)
+    c = _case(D, B, 5, 8, 8, D, 300, loc, 0, False, cuda_device)
+    _memory(c, rng, rng.integers(1, 30, size=2 * B), np.arange(2 * B).reshape(B, 2), cuda_device)
+    clean = _run(msa, c, cuda_device)
+    bad = np.arange(0, B, 3)
+    for x in (float("nan"), float("inf")):
+        for b in bad:
+            c["Vl"][b], c["Vd"][b] = x, x
+            c["Vb"][c["off"][2 * b]:c["off"][2 * b + 2]] = x
+        got = _run(msa, c, cuda_device)
+        good = np.setdiff1d(np.arange(B), bad)
+        assert torch.equal(got[good], clean[good])
+        assert not torch.isfinite(got[bad]).any()
+
+
+def test_calls_side_by_side_and_shared_workspaces(msa, cuda_device):
+    """Two streams at once with workspaces of their own; two shapes back to back, and two graphs, over
+    one workspace."""
+    import torch
+
+    dev = cuda_device
+    t = lambda a: torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+    cs = [_case(31, 2, 24, 16, 4, 64, 900, [900, 333], 3, False, dev), _case(32, 3, 9, 8, 2, 128, 500, [1, 499, 0], 2, True, dev)]
+    args = []
+    for c in cs:
+        kw = dict(n_draft=t(c["n_draft"]), K_bar=c["Kb"], V_bar=c["Vb"], chunk_off=t(c["off"]), topk_idx=t(c["top"]))
+        args.append(((c["dims"], c["q"], c["Kd"], c["Vd"], t(O.pack_mask(c["see"])), c["Kl"], c["Vl"], t(c["loc_len"])), kw))
+    ref = [msa.tree_attend(*a, **kw) for a, kw in args]
+    for c, r in zip(cs, ref):
+        _check(r, c)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cs]
+    got = [[] for _ in cs]
+    for _ in range(8):
+        for i, (a, kw) in enumerate(args):
+            got[i].append(msa.tree_attend(*a, **kw, stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, ref[i]) for i in range(2) for g in got[i])
+    size = max(msa.tree_attend_workspace_size(c["dims"], c["B"], c["M"], c["k"], c["Kl"].shape[1]) for c in cs)
+    ws = torch.full((size + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    for i in (0, 1, 1, 0, 0, 1):
+        a, kw = args[i]
+        assert torch.equal(msa.tree_attend(*a, **kw, ws=ws), ref[i])
+    graphs, outs = [], []
+    for a, kw in args:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(msa.tree_attend(*a, **kw, ws=ws))
+        graphs.append(g)
+    for i in (0, 1, 0, 0, 1, 1):
+        outs[i].zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], ref[i])
+    assert msa.check_device_errors() == 0
+
+
+def test_caches_past_2_31_elements(msa, cuda_device):
+    """Appends, commits and attention at the far end of a cache of 2.5e9 elements.  Keys and values are
+    zero except the last 500: a zero key has weight exp(0), so the exact result is short."""
+    import torch
+
+    dev, B, T, n_kv, D, M, tail = cuda_device, 2, 1_210_000, 8, 128, 3, 500
+    gen = torch.Generator(device=dev).manual_seed(8)
+    rn = lambda *s: torch.randn(*s, generator=gen, device=dev).to(torch.bfloat16)
+    K, V = (torch.zeros(B, T, n_kv, D, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device=dev)
+    L = T - 10
+    K[1, L - tail:L], V[1, L - tail:L] = rn(tail, n_kv, D), rn(tail, n_kv, D)
+    rot = msa.rotary(D)
+    q, k, v = rn(B, 8, D), rn(B, n_kv, D), rn(B, n_kv, D)
+    msa.head_norm_append(rot, q, k, v, None, None, i32(5, L), i32(0, L), K, V)
+    _, kr = msa.head_norm_rotate(rot, q, k, None, None, i32(5, L))
+    assert torch.equal(K[1, L], kr[1]) and torch.equal(V[1, L], v[1]) and torch.equal(K[0, 0], kr[0])
+    Kd, Vd = rn(B, M, n_kv, D), rn(B, M, n_kv, D)
+    new = msa.tree_commit(Kd, Vd, i32(0, 2, 1, 2).view(2, 2), i32(0, 2), K, V, i32(0, L + 1))
+    assert new.tolist() == [0, L + 3]
+    assert torch.equal(K[1, L + 1:L + 3], Kd[1, 1:3]) and torch.equal(V[1, L + 1:L + 3], Vd[1, 1:3])
+    assert float(K[1, L + 3:].abs().sum()) == 0 and float(V[1, :L - tail].abs().max()) == 0
+    d = _dims(16, n_kv, D)
+    see = np.zeros((B, M, M), dtype=bool)
+    see[:, :, 0] = see[:, 2, 1] = True
+    qq = rn(B, M, 16, D)
+    got = msa.tree_attend(d, qq, Kd, Vd, torch.from_numpy(O.pack_mask(see)).to(dev), K, V, new)
+    Kt, Vt = K[1, L - tail:L + 3].double(), V[1, L - tail:L + 3].double()
+    for b, h, r in [(1, 0, 0), (1, 15, 1), (1, 6, 2), (0, 3, 2)]:
+        js = np.nonzero(see[b, r])[0]
+        Kr, Vr = (torch.cat([x[:, h // 2] if b else x[:0, 0], y[b, js][:, h // 2].double()]) for x, y in ((Kt, Kd), (Vt, Vd)))
+        s = Kr @ qq[b, r, h].double() * D ** -0.5
+        w = torch.exp(s - s.max())
+        total = w.sum() + (L - tail if b else 0) * torch.exp(-s.max())  # the zero keys
+        ref, A = w @ Vr / total, w @ Vr.abs() / total
+        assert bool(((got[b, r, h].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + (2.0 ** -8 + 2.0 ** -12) * A).all())
+    assert msa.check_device_errors() == 0
+
+
 # ----------------------------------------------------------------------------
 # plan and commit
 # ----------------------------------------------------------------------------
