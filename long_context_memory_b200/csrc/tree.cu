@@ -314,6 +314,30 @@ __device__ __forceinline__ Cover cover_tail(int n) {  // sizes 1, 8, 32, 128
   return c;
 }
 
+__device__ __forceinline__ uint32_t first_rows(int n) { return n >= 8 ? 0xFFu : n > 0 ? (1u << n) - 1 : 0u; }
+
+// The rows of a value tile that no box brings (lane i < 16 has the bits of the rows 8 i .. that one
+// does) still hold an older tile's, maybe of a query whose values are not finite: zeros.  Called by
+// the producer warp for the last tile of a sequence; out of line, off the other tiles' path.
+template <int DB>
+__device__ __noinline__ void clear_rest(uint8_t* dst, uint32_t bits) {
+  const int lane = threadIdx.x & 31;
+  for (int g = 0; g < kTile / 8; ++g) {
+    const uint32_t m = __shfl_sync(0xffffffffu, bits, g);
+    if (m == 0xFFu) continue;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {  // four rows at once, eight lanes a row of 128 bytes
+      const int r = u * 4 + (lane >> 3);
+      if (!(m >> r & 1))
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          *reinterpret_cast<uint4*>(dst + d * (kTile * 128) + (g * 8 + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_constant__ TreeMaps maps,
                                                                        const __grid_constant__ TreeP p) {
@@ -556,7 +580,6 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         const int kind = t < Tc ? 0 : t < Tc + Tl ? 1 : 2;  // pooled rows, local rows, drafts
         int rows, k_rows;   // rows of the tile; rows that its key and value boxes bring
         int v_rows;
-        uint32_t keep[4];   // rows of the tile that its value boxes bring (uniform over the warp)
         int doc0 = 0;       // kind 0: the first document with keys in the tile
         uint32_t bits = 0;  // kind 2, lane < 16: drafts d0 + 8 lane .. that some draft of the query sees
         if (kind == 0) {
@@ -637,16 +660,8 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           }
           k_rows = kTile;
           v_rows = rows;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) keep[q] = seen[q];
         }
-        if (kind != 2) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int left = rows - 32 * q;
-            keep[q] = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1 : 0u;
-          }
-        }
+#pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           uint64_t* fullb = (kv ? vfull : kfull) + st;
           uint8_t* dst = (kv ? vs : ks) + st * kTB;
@@ -654,21 +669,8 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
             ok = false;
             break;
           }
-          // The rows that no box brings still hold an older tile's, maybe of a query whose values are
-          // not finite: zeros (a slot's first tile finds the ring cleared).
-          if (kv && x >= (uint32_t)p.ring && (keep[0] & keep[1] & keep[2] & keep[3]) != ~0u) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (keep[q] == ~0u) continue;
-#pragma unroll 1
-              for (int r = lane >> 3; r < 32; r += 4)  // eight lanes a row of 128 bytes
-                if (!(keep[q] >> r & 1))
-                  for (int d = 0; d < DB; ++d)
-                    *reinterpret_cast<uint4*>(dst + d * kBlk + (q * 32 + r) * 128 + (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
+          // a slot's first tile finds the ring cleared
+          if (kv && rows < kTile && x >= (uint32_t)p.ring) clear_rest<DB>(dst, kind == 2 ? bits : first_rows(rows - 8 * lane));
           if (lane == 0) mbar_arrive_expect_tx(fullb, (kv ? v_rows : k_rows) * D * 2);
           __syncwarp();
           if (kind == 0) {  // a lane per (document, box, block of 64 elements)
