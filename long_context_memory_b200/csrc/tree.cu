@@ -131,11 +131,15 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // inside bf16's and fp32's range), so that a tile normally touches O in the MMA alone.
 //
 // Keys of a query: its documents' pooled rows one after the other, the local rows, the drafts, each
-// in tiles of 128.  Work is cut evenly: all tiles of all (query, row block, KV head) items in one
-// line, CTA c of N takes tiles c W / N .. (c + 1) W / N (N = the SMs, or W where there are fewer
-// tiles), so ragged batches and single long queries fill the GPU alike; the at most two items that a
-// CTA shares with its neighbours leave partial results and a note for tree_combine_kernel, which
-// merges them.
+// in tiles of 128.  Work is cut evenly: all tiles of all (query, row block) items stand in one line,
+// the same for each KV head; the CTAs form groups of n_kv, a CTA per head, and group c of N takes
+// tiles c W / N .. (c + 1) W / N (N = SMs / n_kv, or W where there are fewer tiles).  So ragged
+// batches and single long queries fill the GPU alike, a group reads whole cache rows at about the
+// same time, and few items are cut: one line over all heads left 4 SMs more at work, but cut nearly
+// every head of a single query in one place more (16 drafts over the 1M-token memory 22 us against 19;
+// 8 queries of one token over 32K local tokens 190 against 184).  The at most two items that a CTA
+// shares with its neighbours leave partial results and a note for tree_combine_kernel, which merges
+// them.
 //
 // A tile's rows arrive by TMA boxes.  A box costs the TMA unit about 55 cycles and 2.3 per row of
 // 128 bytes (measured), so a document's run of rows is covered by at most two boxes, of the largest
@@ -167,7 +171,7 @@ struct TreeP {
   const int32_t *mask, *n_draft, *loc_len, *chunk_off, *topk_idx;
   __nv_bfloat16* out;
   // [2] per item (few items) or per CTA (many): query (-1: nothing to merge), first draft, KV head,
-  // drafts | first and last CTA, first part's slot
+  // drafts | first and last group, first part's slot
   int4* merges;
   int by_item;
   int32_t* sel;      // [B] pooled rows of each query's documents (B > kSmallB)
@@ -454,16 +458,17 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
   auto cost_of = [&](int b) -> long long {
     int sel, L, n;
     query(b, sel, L, n);
-    return (long long)p.n_kv * blocks_of<NT>(p, n) * tiles_of(sel, L, n);
+    return (long long)blocks_of<NT>(p, n) * tiles_of(sel, L, n);
   };
-  // CTA c of the n_act with work begins at tile floor(c total / n_act)
+  // group c of the n_act with work begins at tile floor(c total / n_act)
+  const int group = blockIdx.x / p.n_kv, hk = blockIdx.x - group * p.n_kv;
   long long total = 0, w_begin = 0, w_end = 0;
   int n_act = 1;
   auto begin_of = [&](int c) { return min(total, muldiv(total, c, n_act)); };
   auto cut = [&] {
-    n_act = (int)max(1ll, min((long long)gridDim.x, total));
-    w_begin = begin_of(blockIdx.x);
-    w_end = begin_of(blockIdx.x + 1);
+    n_act = (int)max(1ll, min((long long)(gridDim.x / p.n_kv), total));
+    w_begin = begin_of(group);
+    w_end = begin_of(group + 1);
   };
   if (p.B == 1) {  // (only the producer needs it)
     if (warp == kSoftWarps) {
@@ -536,15 +541,14 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           T = tiles_of(sel, L, n);
           fresh = listed = false;
         }
-        const long long c = (long long)p.n_kv * blocks_of<NT>(p, n) * T;
+        const long long c = (long long)blocks_of<NT>(p, n) * T;
         if (w < bbase + c) break;
         bbase += c;
         ++b;
         fresh = true;
       }
-      const int item = divide(w - bbase, T), lo = (int)(w - bbase - (long long)item * T);
+      const int rb = divide(w - bbase, T), lo = (int)(w - bbase - (long long)rb * T);
       const int hi = (int)min((long long)T, lo + (w_end - w));
-      const int rb = item / p.n_kv, hk = item - rb * p.n_kv;
       const int t0 = rb * NT * p.TT;
       const int Tc = (sel + kTile - 1) / kTile, Tl = (L + kTile - 1) / kTile;
       if (lane == 0) {
@@ -718,13 +722,13 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         }
         if (t == lo && lane == 0 && (p.by_item ? lo == 0 : first && lo > 0)) {
           // the note for the merge: of a cut item by the CTA that begins it (per item), or by the
-          // first CTA that it reaches (per CTA)
-          const long long w0 = w - lo;  // tile w is in the CTA floor(((w + 1) N - 1) / W)
-          const int ca = p.by_item ? (int)blockIdx.x : divide((w0 + 1) * n_act - 1, total);
+          // next group's (per CTA)
+          const long long w0 = w - lo;  // tile w is in the group floor(((w + 1) N - 1) / W)
+          const int ca = p.by_item ? group : divide((w0 + 1) * n_act - 1, total);
           const int cz = divide((w0 + T) * n_act - 1, total);
           const size_t at = p.by_item ? (size_t)(b * p.n_rb + rb) * p.n_kv + hk : (size_t)blockIdx.x;
-          if (p.by_item || ca + 1 == (int)blockIdx.x) {
-            p.merges[2 * at + 1] = make_int4(ca, cz, 2 * ca + (begin_of(ca) == w0 ? 0 : 1), 0);
+          if (p.by_item || ca + 1 == group) {
+            p.merges[2 * at + 1] = make_int4(ca, cz, 2 * (ca * p.n_kv + hk) + (begin_of(ca) == w0 ? 0 : 1), 0);
             p.merges[2 * at] = make_int4(ca == cz ? -1 : b, t0, hk, n);
           }
         }
@@ -861,7 +865,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
       const int* h = hdr[hb];
       const int b = h[kHb];
       if (b < 0) break;
-      const int hk = h[kHhk], sel = h[kHsel], L = h[kHL], n_use = h[kHn], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
+      const int sel = h[kHsel], L = h[kHL], n_use = h[kHn], Tc = h[kHTc], Tl = h[kHTl], lo = h[kHlo],
                 hi = h[kHhi], part = h[kHslot];
       const int rt = r / p.G, g = r - rt * p.G;
       const int t_row = h[kHt0] + i * p.TT + rt;
@@ -1040,7 +1044,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
       for (int u = 0; u < kAhead; ++u) {
         ml[u] = make_float2(-INFINITY, 0.f);
         if (c + u <= c1) {
-          const size_t slot = c + u > c0 ? 2 * (size_t)(c + u) : (size_t)cs.z;
+          const size_t slot = c + u > c0 ? 2 * ((size_t)(c + u) * p.n_kv + it.z) : (size_t)cs.z;
           ml[u] = *reinterpret_cast<const float2*>(p.part_ml + (slot * (NT * 128) + r) * 2);
           o[u] = *reinterpret_cast<const float4*>(p.part_o + ((slot * (D / 4) + e4) * (NT * 128) + r) * 4);
         }
