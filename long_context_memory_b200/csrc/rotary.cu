@@ -7,7 +7,12 @@
 //   gradient  z = Rot^T(dy), u = z (w_off + w): dx = r (u - n mean(u n)), dw = sum z n
 //
 // All of them read each head once and write it once, a few dozen operations per element: bound by
-// HBM at the large sizes and by the launch at the small ones.
+// HBM at the large sizes and by the launch at the small ones.  Measured: the transposed rotation of
+// 8193 rows of 40 fp32 heads of 128 (336 MB) 64.6 us, 5.2 TB/s; norm and rotation of 16384 rows of 40
+// bf16 heads of 128 (336 MB) 70 us, 4.8 TB/s (a plain copy of the same bytes: 55 us; here the issue
+// slots are 53% busy as well); the gradients of 8191 rows of 40 fp16 heads of 96 (189 MB) 62 us, 3.1
+// TB/s, bound by the arithmetic of a head group and its dependences; one row 2.8 us, a decode step of 16
+// rows with its cache 3.4 us on the device, of which the launch is most.
 //
 // Work split.  A head is taken by L lanes (a power of two, 32 / L heads per warp at once); a lane
 // holds one unit of two V-element vectors that contain whole rotation pairs, so that the rotation
@@ -439,7 +444,8 @@ __global__ void __launch_bounds__(256, kRotCtas) rotate_kernel(const __grid_cons
 
 // Gradients of the norms: persistent warps take (row, share) items in a fixed order, the query heads
 // of all of them and then the key heads, and keep the weight gradients of their lanes' elements in
-// registers; a CTA sums its warps in order and writes one partial per weight.
+// registers; a CTA sums its warps in order and writes one partial per weight.  The next batch is not
+// loaded ahead: that needs 168 registers, so 12 warps per SM instead of 16 (80 us against 62).
 //   z = Rot^T(dy), u = z w, n = x r:  dx = r u - (r^2 mean(u n)) x,  dw += z n
 template <typename T, int V, int J, bool INTER>
 __global__ void __launch_bounds__(256, kGradCtas) norm_grad_kernel(const __grid_constant__ RotP p) {
