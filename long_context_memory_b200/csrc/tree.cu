@@ -156,8 +156,8 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 //
 // Measured (heads of 128, 32 query and 8 KV heads): 16 drafts of one query over 16 documents and 4K
 // local tokens 19.8 us, bound by the chain of a CTA's two to three tiles and the merge; 32 queries of 32
-// drafts over 8K tokens (1.17 GB) 246 us, 4.8 TB/s, on inputs that were not used just before, 212-220 us (5.4) on
-// such that were; 64 drafts of 32 queries 292 us, 940 TFLOP/s.  Heads of 64, 7 queries of up to 127 drafts over up
+// drafts over 8K tokens (1.17 GB) 246-261 us, 4.5-4.8 TB/s, on inputs that were not used just before, 212-220 us (5.4)
+// on such that were; 64 drafts of 32 queries 292 us, 940 TFLOP/s.  Heads of 64, 7 queries of up to 127 drafts over up
 // to 20K tokens: 59-72 us, bound by the softmax threads (about 3,050 cycles per key tile and two row
 // tiles, of which the weights take 1,700; a polynomial for a fifth to a third of the exponentials made it slower).
 // ---------------------------------------------------------------------------
