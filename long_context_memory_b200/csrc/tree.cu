@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "tree_notes.h"
 
 namespace msa {
 
@@ -186,7 +187,7 @@ struct TreeP {
   int32_t* sel;      // [B] pooled rows of each query's documents (B > kSmallB)
   float* part_o;     // [2 N][D / 4][NT * 128][4] unnormalised (a warp's rows side by side)
   float* part_ml;    // [2 N][NT * 128][2] reference maximum, sum
-  int B, M, W, n_q, n_kv, G, TT, n_rb, t_loc_max, n_docs, n_chunks, k, ring, pad;
+  int B, M, W, n_q, n_kv, G, TT, n_rb, t_loc_max, n_docs, n_chunks, k, ring, pad, groups;
   float scale_log2;
 };
 
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
   int n_act = 1;
   auto begin_of = [&](int c) { return min(total, muldiv(total, c, n_act)); };
   auto cut = [&] {
-    n_act = (int)max(1ll, min((long long)(gridDim.x / p.n_kv), total));
+    n_act = (int)max(1ll, min((long long)p.groups, total));
     w_begin = begin_of(group);
     w_end = begin_of(group + 1);
   };
@@ -1048,7 +1049,8 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
 // The items that several CTAs of tree_attend_kernel shared: their parts merged in CTA order.  A CTA
 // takes 1024 / D rows of the item noted by one CTA, a thread 4 elements of a row, neighbouring
 // threads neighbouring rows (as the parts lie); the parts are read once, kAhead of them in flight,
-// with a running maximum.
+// with a running maximum.  A note that no call of these sizes leaves (an attention kernel that gave up
+// before it wrote it, which is reported) is passed over.
 template <int D, int NT, int kAhead>
 __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant__ TreeP p) {
   constexpr int kRows = 1024 / D;
@@ -1059,7 +1061,7 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const __grid_constant
   }
   const int4 it = p.merges[2 * blockIdx.y], cs = p.merges[2 * blockIdx.y + 1];
   const int b = it.x, n = it.w, c0 = cs.x, c1 = cs.y;
-  if (b < 0) return;
+  if (!merge_note_ok({b, it.y, it.z, n, c0, c1, cs.z}, p.B, p.M, p.n_kv, p.groups)) return;
   const int r = blockIdx.x * kRows + (threadIdx.x & (kRows - 1)), e4 = threadIdx.x / kRows;  // row of the block, elements 4 e4 ..
   const int i = r >> 7, rt = (r & 127) / p.G, g = (r & 127) - rt * p.G;
   const int t = it.y + i * p.TT + rt;
@@ -1137,6 +1139,7 @@ cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), (int)room);
   if (e != cudaSuccess) return e;
   const int n_ctas = sm_count();
+  p.groups = n_ctas / p.n_kv;
   {
     TraceScope ts(kKTreeAttend, s);
     e = launch_pdl(kern, dim3(n_ctas), dim3(320), smem, s, maps, p);

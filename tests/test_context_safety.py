@@ -1,0 +1,86 @@
+"""Host-side tests of what the rotation, norm and draft-tree calls do with what they cannot use: notes
+that were never written, truth values that raise, sizes that do not fit, tensors that overlap (no GPU)."""
+import os
+import subprocess
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "long_context_memory_b200", "csrc")
+
+NOTES = r"""
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <random>
+#include "tree_notes.h"
+
+// The merge's loads and stores for a note, as tree_combine_kernel makes them: parts slot by slot,
+// output rows of a block of up to `nt` row tiles of `tt` drafts.
+static bool inside(const msa::MergeNote& n, int B, int M, int n_kv, int G, int tt, int nt, int ctas) {
+  if (n.last - (int64_t)n.first > ctas) return false;  // the loop over the parts ends
+  for (int64_t c = n.first; c <= n.last; ++c) {
+    const int64_t slot = c > n.first ? 2 * (c * n_kv + n.head) : n.slot;
+    if (slot < 0 || slot >= 2 * ctas) return false;
+  }
+  const int64_t rows = (int64_t)B * M * n_kv * G;
+  for (int64_t i = 0; i < (int64_t)nt * tt; ++i) {
+    const int64_t t = n.draft + i;
+    if (t >= M) break;  // the kernel returns
+    for (int g = 0; g < G; ++g) {
+      const int64_t row = ((int64_t)n.query * M + t) * n_kv * G + (int64_t)n.head * G + g;
+      if (t < 0 || row < 0 || row >= rows) return false;
+    }
+  }
+  return true;
+}
+
+int main() {
+  std::mt19937 rng(7);
+  const int sizes[][4] = {{1, 1, 1, 1}, {8, 16, 8, 4}, {8, 200, 8, 4}, {4096, 256, 1, 16}, {33, 5, 3, 7}, {2, 255, 7, 2}};
+  long passed = 0, real = 0;
+  for (auto& s : sizes)
+    for (int ctas : {8, 132, 148}) {
+      const int B = s[0], M = s[1], n_kv = s[2], G = s[3], tt = 128 / G, nt = M > tt ? 2 : 1, groups = ctas / n_kv;
+      auto note = [&](const int32_t (&v)[7]) { return msa::MergeNote{v[0], v[1], v[2], v[3], v[4], v[5], v[6]}; };
+      auto ok = [&](const msa::MergeNote& n) { return msa::merge_note_ok(n, B, M, n_kv, groups); };
+      const int32_t edge[] = {0, 1, -1, 2, B - 1, B, M - 1, M, n_kv - 1, n_kv, groups - 1, groups, ctas, 2 * ctas - 1, 2 * ctas,
+                              INT32_MAX, INT32_MIN, 0x7F7F7F7F, (int32_t)0xFEFEFEFE, 1 << 30};
+      for (int it = 0; it < 300000; ++it) {
+        int32_t v[7];
+        for (int32_t& x : v) x = rng() % 3 == 0 ? (int32_t)rng() : edge[rng() % (sizeof(edge) / sizeof(edge[0]))];
+        if (rng() % 4 == 0) v[6] = 2 * (int32_t)((uint32_t)v[4] * (uint32_t)n_kv + (uint32_t)v[2]) + (int)(rng() % 2);
+        if (!ok(note(v))) continue;
+        ++passed;
+        if (!inside(note(v), B, M, n_kv, G, tt, nt, ctas)) {
+          printf("a note outside its buffers passed: %d %d %d %d %d %d %d\n", v[0], v[1], v[2], v[3], v[4], v[5], v[6]);
+          return 1;
+        }
+      }
+      for (int c = 0; c + 1 < groups; ++c)  // what the kernel writes for a cut item
+        for (int h = 0; h < n_kv; ++h)
+          for (int last = c + 1; last < groups; ++last)
+            for (int second = 0; second < 2; ++second, ++real)
+              if (!ok({B - 1, (M - 1) / (nt * tt) * nt * tt, h, M, c, last, 2 * (c * n_kv + h) + second}) || ok({-1, 0, h, M, c, last, 2 * (c * n_kv + h)})) {
+                printf("a real note was refused\n");
+                return 1;
+              }
+    }
+  printf("%ld %ld\n", passed, real);
+  return passed > 100 && real > 1000 ? 0 : 1;
+}
+"""
+
+
+def test_merge_notes_that_nobody_wrote_stay_inside_their_buffers(tmp_path):
+    """The merge of a draft-tree attention after a CTA gave up waiting: whatever the workspace held in the
+    place of its note, a note that the merge takes indexes nothing outside the parts and the output."""
+    src, exe = tmp_path / "notes.cpp", tmp_path / "notes"
+    src.write_text(NOTES)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+    # and the kernel asks before it uses one
+    text = open(os.path.join(CSRC, "tree.cu"), encoding="utf-8").read()
+    merge = text[text.index("tree_combine_kernel(const"):text.index("// drafts per row tile")]
+    assert merge.index("merge_note_ok(") < min(merge.index("p.part_ml"), merge.index("p.out +"))
