@@ -746,6 +746,7 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
           }
           __syncwarp();
         }
+        if (!ok) break;  // this tile's values were not asked for: x counts those that were
         if (++st == p.ring) {
           st = 0;
           ph ^= 1;
