@@ -295,6 +295,7 @@ __global__ void __launch_bounds__(256) tree_select_kernel(const int32_t* __restr
   for (int r = lane; r < k; r += 32) {
     const int doc = topk_idx[(size_t)b * k + r];
     if (doc >= 0 && doc < n_docs) g += max(0, min(chunk_off[doc + 1] - chunk_off[doc], n_chunks));
+    else raise_dev_error(kDevErrBadIndex);  // (the attention lists only documents of queries with tiles)
   }
   g = __reduce_add_sync(0xffffffffu, g);
   if (lane == 0) sel[b] = g;
