@@ -63,6 +63,7 @@ enum KernelId : int {
   kKTreeAttend,
   kKTreeCombine,
   kKTreeCommit,
+  kKTreeSelect,
   kKernelCount
 };
 

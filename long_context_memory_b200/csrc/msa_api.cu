@@ -233,7 +233,8 @@ const char* kKernelNames[kKernelCount] = {
     "router_query", "scan", "topk_slice", "topk_merge", "rope_table", "attn_split", "attn_combine",
     "enc_chunk_map", "enc_transpose_w", "enc_gemm_k", "enc_pool_h", "enc_gemm_pooled", "rope_rows", "gather_plan", "gather_copy",
     "chunk_off_extend", "aux_loss", "kv_append", "kr_norms", "attn_merge", "chunk_doc",
-    "rotate", "head_norm", "head_norm_grad", "head_norm_sum", "tree_plan", "tree_attend", "tree_combine", "tree_commit"};
+    "rotate", "head_norm", "head_norm_grad", "head_norm_sum", "tree_plan", "tree_attend", "tree_combine", "tree_commit",
+    "tree_select"};
 
 struct TraceState {
   std::mutex mu;

@@ -1259,7 +1259,7 @@ msa_status tree_attend_launch(const msa_dims& d, const TreeAttendCall& c, cudaSt
   for (int i = 0; i < 2 && st == MSA_OK; ++i) st = map4(&maps.v_draft[i], c.V_draft, d.n_kv, c.M, row, 1, kTailRows[i]);
   if (st != MSA_OK) return st;
   if (c.k > 0 && c.B > kSmallB) {
-    TraceScope ts(kKTreePlan, s);
+    TraceScope ts(kKTreeSelect, s);
     MSA_CUDA_CHECK(launch_pdl(tree_select_kernel, dim3((c.B + 7) / 8), dim3(256), 0, s, c.topk_idx, c.chunk_off, c.B,
                               c.k, c.n_docs, c.n_chunks, w.sel));
   }
