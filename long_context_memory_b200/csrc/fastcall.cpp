@@ -145,6 +145,17 @@ long long integer(PyObject* o) {
   return v;
 }
 
+// The library's call without the interpreter's lock: a launch may have to wait (for a place in the
+// stream's queue, for the first load of a kernel), and what the queue waits for may be a host function that
+// needs the interpreter.  Nothing of Python is touched meanwhile: the arguments are read before.
+template <typename F, typename... A>
+long unlocked(F f, A... a) {
+  PyThreadState* state = PyEval_SaveThread();
+  const msa_status st = f(a...);
+  PyEval_RestoreThread(state);
+  return st;
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
   if (got != want) {
@@ -187,8 +198,8 @@ PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     msa_heads k{};
     if (a[3] != Py_None) k = r.call.heads(tensor(a[3], "k"), &tensor(a[6], "k_out"), "k", r.rows, D, r.type);
     r.call.on_current_device("q");
-    return entry.rotate(rot.get(), r.code, &q, a[3] != Py_None ? &k : nullptr, r.rows, r.pos, PyObject_IsTrue(a[4]),
-                        r.call.stream(a[7]));
+    return unlocked(entry.rotate, rot.get(), r.code, &q, a[3] != Py_None ? &k : nullptr, r.rows, r.pos,
+                    PyObject_IsTrue(a[4]), r.call.stream(a[7]));
   });
 }
 
@@ -205,8 +216,8 @@ PyObject* py_head_norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* wk = r.call.flat_or_null(a[4], "k_weight", {D}, r.type);
     const float eps = (float)number(a[6]), off = (float)number(a[7]);
     r.call.on_current_device("q");
-    return entry.head_norm_rotate(rot.get(), r.code, &q, a[2] != Py_None ? &k : nullptr, r.rows, wq, wk, off, eps, r.pos,
-                                  r.call.stream(a[10]));
+    return unlocked(entry.head_norm_rotate, rot.get(), r.code, &q, a[2] != Py_None ? &k : nullptr, r.rows, wq, wk, off,
+                    eps, r.pos, r.call.stream(a[10]));
   });
 }
 
@@ -230,8 +241,8 @@ PyObject* py_head_norm_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* V = r.call.flat(a[9], "V_loc", cache, r.type);
     const float eps = (float)number(a[10]), off = (float)number(a[11]);
     r.call.on_current_device("q");
-    return entry.head_norm_append(rot.get(), r.code, &q, &k, &v, r.rows, wq, wk, off, eps, r.pos, slots, K, V,
-                                  (int32_t)cache[0], (int32_t)cache[1], r.call.stream(a[13]));
+    return unlocked(entry.head_norm_append, rot.get(), r.code, &q, &k, &v, r.rows, wq, wk, off, eps, r.pos, slots, K, V,
+                    (int32_t)cache[0], (int32_t)cache[1], r.call.stream(a[13]));
   });
 }
 
@@ -274,8 +285,8 @@ PyObject* py_head_norm_rotate_grad(PyObject*, PyObject* const* a, Py_ssize_t n) 
     workspace(a[14], &ws, &bytes);
     if (tensor(a[14], "ws").device() != r.call.dev) refuse("ws: expected on %s", r.call.dev.str().c_str());
     r.call.on_current_device("q");
-    return entry.head_norm_rotate_grad(rot.get(), r.code, &q, has_k ? &k : nullptr, &dq, has_k ? &dk : nullptr, r.rows, wq,
-                                       wk, off, eps, r.pos, gwq, gwk, ws, bytes, r.call.stream(a[15]));
+    return unlocked(entry.head_norm_rotate_grad, rot.get(), r.code, &q, has_k ? &k : nullptr, &dq,
+                    has_k ? &dk : nullptr, r.rows, wq, wk, off, eps, r.pos, gwq, gwk, ws, bytes, r.call.stream(a[15]));
   });
 }
 
@@ -294,7 +305,7 @@ PyObject* py_tree_plan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const long long off = integer(a[2]);
     if (off < 0 || off > INT32_MAX) refuse("pos_offset: expected an int32 >= 0, got %lld", off);
     c.on_current_device("parents");
-    return entry.tree_plan(par, nd, loc, (int32_t)B, (int32_t)M, (int32_t)off, mask, pos, c.stream(a[6]));
+    return unlocked(entry.tree_plan, par, nd, loc, (int32_t)B, (int32_t)M, (int32_t)off, mask, pos, c.stream(a[6]));
   });
 }
 
@@ -357,8 +368,9 @@ PyObject* py_tree_attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
     workspace(a[15], &ws, &bytes);
     if (tensor(a[15], "ws").device() != c.dev) refuse("ws: expected on %s", c.dev.str().c_str());
     c.on_current_device("q");
-    return entry.tree_attend(d.get(), qp, kd, vd, mask, nd, (int32_t)B, (int32_t)M, kl, vl, loc, (int32_t)t_loc, kb, vb, co,
-                             (int32_t)n_docs, (int32_t)n_chunks, top, (int32_t)k, scale, out, ws, bytes, c.stream(a[16]));
+    return unlocked(entry.tree_attend, d.get(), qp, kd, vd, mask, nd, (int32_t)B, (int32_t)M, kl, vl, loc,
+                    (int32_t)t_loc, kb, vb, co, (int32_t)n_docs, (int32_t)n_chunks, top, (int32_t)k, scale, out, ws,
+                    bytes, c.stream(a[16]));
   });
 }
 
@@ -387,8 +399,8 @@ PyObject* py_tree_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     d.n_r = 1;
     d.d_r = d.chunk = 64;
     d.rope_base = 1e6f;
-    return entry.tree_commit(&d, kp, vp, pp, np, (int32_t)B, (int32_t)M, (int32_t)A, K, V, loc, (int32_t)T, out,
-                             c.stream(a[8]));
+    return unlocked(entry.tree_commit, &d, kp, vp, pp, np, (int32_t)B, (int32_t)M, (int32_t)A, K, V, loc, (int32_t)T,
+                    out, c.stream(a[8]));
   });
 }
 
