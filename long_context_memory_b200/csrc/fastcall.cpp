@@ -156,6 +156,12 @@ long unlocked(F f, A... a) {
   return st;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Refused("");
+  return v != 0;
+}
+
 template <typename F>
 PyObject* guarded(Py_ssize_t got, Py_ssize_t want, F&& f) {
   if (got != want) {
@@ -197,9 +203,10 @@ PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const msa_heads q = r.call.heads(r.q, &tensor(a[5], "out"), "q", r.rows, D, r.type);
     msa_heads k{};
     if (a[3] != Py_None) k = r.call.heads(tensor(a[3], "k"), &tensor(a[6], "k_out"), "k", r.rows, D, r.type);
+    const bool grad = truth(a[4]);
     r.call.on_current_device("q");
-    return unlocked(entry.rotate, rot.get(), r.code, &q, a[3] != Py_None ? &k : nullptr, r.rows, r.pos,
-                    PyObject_IsTrue(a[4]), r.call.stream(a[7]));
+    return unlocked(entry.rotate, rot.get(), r.code, &q, a[3] != Py_None ? &k : nullptr, r.rows, r.pos, (int32_t)grad,
+                    r.call.stream(a[7]));
   });
 }
 

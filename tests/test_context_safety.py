@@ -84,3 +84,23 @@ def test_merge_notes_that_nobody_wrote_stay_inside_their_buffers(tmp_path):
     text = open(os.path.join(CSRC, "tree.cu"), encoding="utf-8").read()
     merge = text[text.index("tree_combine_kernel(const"):text.index("// drafts per row tile")]
     assert merge.index("merge_note_ok(") < min(merge.index("p.part_ml"), merge.index("p.out +"))
+
+
+@pytest.fixture(scope="module")
+def msa():
+    from long_context_memory_b200 import build
+
+    if build.needs_build():
+        build.build()
+    import long_context_memory_b200 as m
+
+    return m
+
+
+def test_a_truth_value_that_raises_is_passed_on(msa):
+    """rotate's ``grad`` is read before anything is launched, and its error is the caller's."""
+    import torch
+
+    q, pos = torch.zeros(2, 3, 64), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        msa.rotate(msa.rotary(64), q, pos, grad=torch.zeros(2))
