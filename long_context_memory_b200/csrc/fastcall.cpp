@@ -90,6 +90,7 @@ struct Call {
       refuse("%s: expected [%lld, heads, %lld] %s on %s with contiguous head elements, got %s %s on %s, strides %s", name,
              (long long)rows, (long long)head_dim, c10::toString(type), dev.str().c_str(), text(x.sizes()).c_str(),
              c10::toString(x.scalar_type()), x.device().str().c_str(), text(x.strides()).c_str());
+    if (x.size(1) > INT32_MAX) refuse("%s: expected fewer than 2^31 heads, got %lld", name, (long long)x.size(1));
     msa_heads h{};
     h.in = x.data_ptr();
     h.in_row = x.stride(0);

@@ -104,3 +104,18 @@ def test_a_truth_value_that_raises_is_passed_on(msa):
     q, pos = torch.zeros(2, 3, 64), torch.zeros(2, dtype=torch.int32)
     with pytest.raises(RuntimeError, match="ambiguous"):
         msa.rotate(msa.rotary(64), q, pos, grad=torch.zeros(2))
+
+
+def test_heads_beyond_32_bits_are_refused(msa):
+    """2^32 + 1 heads (of a broadcast tensor) are not one head."""
+    import torch
+
+    q = torch.zeros(1, 1, 64).expand(1, 2 ** 32 + 1, 64)
+    out = torch.zeros(1, 1, 64).expand(1, 2 ** 32 + 1, 64)
+    pos = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(ValueError, match="heads"):
+        msa.rotate(msa.rotary(64), q, pos, out=out)
+    with pytest.raises(ValueError, match="heads"):
+        msa.head_norm_rotate(msa.rotary(64), q, None, None, None, pos, out=out)
+    with pytest.raises(ValueError, match="CUDA"):  # what fits is told that it wants CUDA tensors
+        msa.rotate(msa.rotary(64), q[:, :3], pos)
