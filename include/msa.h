@@ -571,7 +571,8 @@ msa_status msa_rope_cache_build(const msa_dims* dims, int32_t t_loc_max, int32_t
  * msa_heads: `heads` heads of each of the call's rows; element (row, head, d) is
  * at in + row * in_row + head * in_head + d, strides in elements (a slice of a
  * fused projection works), and likewise out.  out may equal in with the same
- * strides; otherwise they must not overlap.  Pointers need the alignment of an
+ * strides; otherwise they must not overlap (refused).  Outputs and inputs of different
+ * msa_heads of a call must not overlap either.  Pointers need the alignment of an
  * element only; the kernels take 16-byte accesses where pointers, strides and
  * rot_dim allow them.
  * dtype: type of every head tensor and weight of the call.

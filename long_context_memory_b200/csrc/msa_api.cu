@@ -16,6 +16,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "overlap.h"
 
 namespace msa {
 
@@ -942,8 +943,13 @@ static msa_status check_heads(const msa_heads* h, const char* name, const msa_ro
                                      : h->out_head >= h->out_row * (rows - 1) + D;
     if (!ok) return fail(MSA_ERR_INVALID_ARG, "%s: output heads overlap (strides %lld, %lld)", name,
                          (long long)h->out_row, (long long)h->out_head);
-    if (needs_in && h->in == h->out && ((many_r && h->in_row != h->out_row) || (many_h && h->in_head != h->out_head)))
-      return fail(MSA_ERR_INVALID_ARG, "%s: an in-place call needs equal strides", name);
+    const int64_t step = (int64_t)size;
+    const Blocks to{reinterpret_cast<uintptr_t>(h->out), rows, h->heads, h->out_row * step, h->out_head * step, D * step};
+    if (needs_in) {
+      const Blocks from{reinterpret_cast<uintptr_t>(h->in), rows, h->heads, h->in_row * step, h->in_head * step, D * step};
+      if (!same_blocks(from, to) && share_bytes(from, to))
+        return fail(MSA_ERR_INVALID_ARG, "%s: out overlaps in, and is not in with the same strides", name);
+    }
   }
   return MSA_OK;
 }

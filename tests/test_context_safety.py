@@ -1,6 +1,7 @@
 """Host-side tests of what the rotation, norm and draft-tree calls do with what they cannot use: notes
 that were never written, truth values that raise, sizes that do not fit, tensors that overlap (no GPU)."""
 import os
+import struct
 import subprocess
 
 import pytest
@@ -119,3 +120,114 @@ def test_heads_beyond_32_bits_are_refused(msa):
         msa.head_norm_rotate(msa.rotary(64), q, None, None, None, pos, out=out)
     with pytest.raises(ValueError, match="CUDA"):  # what fits is told that it wants CUDA tensors
         msa.rotate(msa.rotary(64), q[:, :3], pos)
+
+
+SHARE = r"""
+#include <cstdio>
+#include <random>
+#include <set>
+#include <vector>
+#include "overlap.h"
+using msa::Blocks;
+static std::vector<char> bytes(const Blocks& t) {
+  std::vector<char> v(6000, 0);
+  for (int r = 0; r < t.rows; ++r)
+    for (int h = 0; h < t.heads; ++h)
+      for (int e = 0; e < t.width; ++e) v[t.base + r * t.row + h * t.head + e] = 1;
+  return v;
+}
+int main() {
+  std::mt19937 rng(11);
+  auto u = [&](int n) { return (int64_t)(rng() % n); };
+  long shared = 0, apart = 0, careful = 0;
+  for (int it = 0; it < 200000; ++it) {
+    Blocks a, b;
+    const int64_t pitch = 1 + u(60), head = 1 + u(30);
+    for (Blocks* t : {&a, &b}) {
+      *t = {(uintptr_t)u(400), 1 + u(6), 1 + u(6), u(4) ? pitch * (1 + (u(3) == 0)) : u(120), u(4) ? head : u(60), 1 + u(12)};
+      if (u(8) == 0) std::swap(t->row, t->head);
+    }
+    const std::vector<char> va = bytes(a), vb = bytes(b);
+    bool truth = false;
+    for (size_t i = 0; i < va.size(); ++i) truth |= va[i] && vb[i];
+    const bool got = msa::share_bytes(a, b);
+    if (got != msa::share_bytes(b, a)) return printf("not symmetric\n"), 1;
+    if (truth && !got) return printf("a shared byte was missed\n"), 1;
+    auto one = [](int64_t n, int64_t s, int64_t m, int64_t t) { return n == 1 || s == 0 || m == 1 || t == 0 || s == t; };
+    const bool exact = one(a.rows, a.row, b.rows, b.row) || one(a.heads, a.head, b.heads, b.head);
+    if (exact && got != truth) return printf("tensors apart were taken for sharing\n"), 1;
+    ++(truth ? shared : got ? careful : apart);
+  }
+  // sizes of real calls: slices of a fused projection, head-major and interleaved heads, far rows
+  auto T = [](int64_t base, int64_t rows, int64_t heads, int64_t row, int64_t head, int64_t width) { return Blocks{(uintptr_t)base, rows, heads, row, head, width}; };
+  const int64_t W = 256, R = 48 * W, N = 1 << 30;
+  struct { Blocks a, b; bool share; } real[] = {
+      {T(0, N, 32, R, W, W), T(32 * W, N, 8, R, W, W), false},         // q and k of one projection
+      {T(0, N, 32, R, W, W), T(32 * W - 2, N, 8, R, W, W), true},
+      {T(R, N, 32, R, W, W), T(40 * W, N, 8, R, W, W), false},
+      {T(0, N, 32, R, W, W), T(R, N, 32, R, W, W), true},              // one row off
+      {T(0, N, 16, 48 * W, 3 * W, W), T(W, N, 16, 48 * W, 3 * W, W), false},  // q, k, v of a head side by side
+      {T(0, N, 16, 48 * W, 3 * W, W), T(2 * W + 2, N, 16, 48 * W, 3 * W, W), true},
+      {T(0, N, 32, W, N * W, W), T(32 * N * W, N, 8, W, N * W, W), false},    // head-major
+      {T(0, N, 32, W, N * W, W), T(31 * N * W, N, 8, W, N * W, W), true},
+      {T(0, 1, 32, 7, W, W), T(16 * W, N, 1, R, 9, W), true},
+      {T(1 << 20, INT64_C(2147483647), 65535, INT64_MAX, INT64_MAX, W), T(0, 1, 1, 0, 0, 1 << 20), false},
+      {T(0, 0, 4, R, W, W), T(0, 3, 4, R, W, W), false}};
+  for (auto& c : real)
+    if (msa::share_bytes(c.a, c.b) != c.share || msa::share_bytes(c.b, c.a) != c.share) return printf("case %ld\n", (long)(&c - real)), 1;
+  printf("%ld %ld %ld\n", shared, apart, careful);
+  return shared > 1000 && apart > 1000 ? 0 : 1;
+}
+"""
+
+
+def test_share_bytes_against_enumeration(tmp_path):
+    """The overlap check of two strided tensors against their bytes, one by one."""
+    src, exe = tmp_path / "share.cpp", tmp_path / "share"
+    src.write_text(SHARE)
+    subprocess.run(["g++", "-O2", "-std=c++17", "-Wall", "-Wextra", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+FAKE = 0x100000  # 16-byte aligned non-null "device" address; never dereferenced
+
+
+def _heads(heads, D, inp, out, in_row, in_head, out_row, out_head):
+    return struct.pack("@PPqqqqii", inp, out, in_row, in_head, out_row, out_head, heads, 0)
+
+
+@pytest.mark.parametrize("form", ["rotate", "forward", "backward"])
+@pytest.mark.parametrize("dtype,size", [(0, 2), (2, 4)])
+def test_an_output_that_overlaps_its_input_is_refused(msa, monkeypatch, form, dtype, size):
+    """In place, or apart: an output some rows, heads or elements off its input would be read after it was
+    written.  Outputs that interleave with their input share nothing and are taken."""
+    monkeypatch.setenv("MSA_FAULT", "launch")  # valid calls stop with MSA_ERR_CUDA before their first launch
+    import ctypes
+
+    D, heads, rows = 64, 4, 10
+    r, far = msa.rotary(D), FAKE + (1 << 40)
+
+    def call(off, strides_in, strides_out):
+        h = _heads(heads, D, FAKE, FAKE + off * size, *strides_in, *strides_out)
+        if form == "rotate":
+            return msa.lib.msa_rotate(ctypes.byref(r), dtype, h, None, rows, far, 0, None)
+        if form == "forward":
+            return msa.lib.msa_head_norm_rotate(ctypes.byref(r), dtype, h, None, rows, None, None, 0.0, 1e-6, far, None)
+        x = _heads(heads, D, far, far, *strides_in, *strides_in)
+        return msa.lib.msa_head_norm_rotate_grad(ctypes.byref(r), dtype, x, None, h, None, rows, None, None, 0.0, 1e-6, far,
+                                                 None, None, far, 1 << 24, None)
+
+    flat, wide = (heads * D, D), (2 * heads * D, D)
+    for off in (0, rows * heads * D, 1 << 30):  # in place; right behind; far away
+        assert call(off, flat, flat) == 4
+    for off in (1, 8, D, heads * D, 3 * heads * D, rows * heads * D - 1):
+        assert call(off, flat, flat) == 1, off
+    assert call(0, flat, wide) == 1                    # in place with another pitch
+    assert call(0, (D, rows * D), flat) == 1           # in place, the heads' order turned round
+    assert call(heads * D, wide, wide) == 4            # the other half of every row
+    assert call(heads * D - 1, wide, wide) == 1
+    assert call(heads * D + 1, wide, wide) == 1
+    assert call(D, (8 * D, 2 * D), (8 * D, 2 * D)) == 4  # heads side by side
+    assert call(0, (0, 0), flat) == 1                  # a broadcast input inside its output
+    assert call(heads * D, (0, 0), flat) == 4
