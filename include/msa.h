@@ -641,7 +641,8 @@ msa_status msa_head_norm_append(const msa_rotary* rot, msa_dtype dtype, const ms
  *   z = Rot^T(dy),  u = z (weight_offset + w),  n = x r,  r = 1 / sqrt(mean(x^2) + eps)
  *   dx = r (u - n mean_d(u n)),  dw_d = sum over rows and heads of z_d n_d.
  * q->out and k->out are unused; dq->heads == q->heads.  dq_weight, dk_weight: [head_dim] fp32 device out,
- * each optional (NULL).  k and dk may be NULL together.  The weight sums are taken in a fixed order:
+ * each optional (NULL).  dq->out may also be q->in, and dk->out k->in, with the same strides.
+ * k and dk may be NULL together.  The weight sums are taken in a fixed order:
  * two calls with the same arguments give the same bits on the same GPU.
  * ws >= msa_head_norm_grad_workspace_size(...) bytes, 256-byte aligned. */
 size_t msa_head_norm_grad_workspace_size(const msa_rotary* rot, int64_t rows, int32_t n_q, int32_t n_k);

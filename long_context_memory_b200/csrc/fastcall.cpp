@@ -16,6 +16,7 @@
 #include <string>
 
 #include "../../include/msa.h"
+#include "overlap.h"
 
 namespace {
 
@@ -118,6 +119,47 @@ msa_dtype dtype_of(const at::Tensor& t, const char* name) {
   }
 }
 
+// What the tensors of one call may share: an output nothing with another output or input (but with its
+// own input in place, which the library checks).  Kernels of many CTAs would read what others have written.
+struct Place : msa::Blocks {  // and the bytes that it reaches over (a tensor lies in one allocation: 64 bits hold them)
+  uintptr_t end;
+  Place(const void* p, int64_t rows, int64_t heads, int64_t row, int64_t head, int64_t width)
+      : Blocks{reinterpret_cast<uintptr_t>(p), rows, heads, row, head, width},
+        end(p && rows > 0 ? base + (rows - 1) * row + (heads - 1) * head + width : base) {}
+};
+struct Apart {
+  int64_t rows, head_dim, size;
+  Place in(const msa_heads& h) const {
+    return {h.in, rows, h.heads, h.in_row * size, h.in_head * size, head_dim * size};
+  }
+  Place out(const msa_heads& h) const {
+    return {h.out, rows, h.heads, h.out_row * size, h.out_head * size, head_dim * size};
+  }
+  static Place vec(const void* p, int64_t bytes) { return {p, 1, 1, 0, 0, bytes}; }  // nothing where p is null
+  static void check(const Place& written, const char* name, const Place& other, const char* other_name) {
+    if (written.base < other.end && other.base < written.end && msa::share_bytes(written, other))
+      refuse("%s and %s overlap: expected tensors apart", name, other_name);
+  }
+  // an output against the small inputs of the call
+  void small(const Place& written, const char* name, const void* positions, const void* q_weight,
+             const void* k_weight) const {
+    check(written, name, vec(positions, rows * 4), "positions");
+    check(written, name, vec(q_weight, head_dim * size), "q_weight");
+    check(written, name, vec(k_weight, head_dim * size), "k_weight");
+  }
+  // the outputs of the query and key heads (k.heads == 0: none)
+  void pair(const msa_heads& q, const msa_heads& k, const void* positions, const void* q_weight, const void* k_weight) const {
+    const Place q_out = out(q);
+    small(q_out, "out", positions, q_weight, k_weight);
+    if (!k.heads) return;
+    const Place k_out = out(k);
+    small(k_out, "k_out", positions, q_weight, k_weight);
+    check(q_out, "out", in(k), "k");
+    check(k_out, "k_out", in(q), "q");
+    check(q_out, "out", k_out, "k_out");
+  }
+};
+
 // a ctypes structure by its buffer
 template <typename S>
 struct Struct {
@@ -205,6 +247,7 @@ PyObject* py_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     msa_heads k{};
     if (a[3] != Py_None) k = r.call.heads(tensor(a[3], "k"), &tensor(a[6], "k_out"), "k", r.rows, D, r.type);
     const bool grad = truth(a[4]);
+    Apart{r.rows, D, r.q.element_size()}.pair(q, k, r.pos, nullptr, nullptr);
     r.call.on_current_device("q");
     return unlocked(entry.rotate, rot.get(), r.code, &q, a[3] != Py_None ? &k : nullptr, r.rows, r.pos, (int32_t)grad,
                     r.call.stream(a[7]));
@@ -223,6 +266,7 @@ PyObject* py_head_norm_rotate(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const void* wq = r.call.flat_or_null(a[3], "q_weight", {D}, r.type);
     const void* wk = r.call.flat_or_null(a[4], "k_weight", {D}, r.type);
     const float eps = (float)number(a[6]), off = (float)number(a[7]);
+    Apart{r.rows, D, r.q.element_size()}.pair(q, k, r.pos, wq, wk);
     r.call.on_current_device("q");
     return unlocked(entry.head_norm_rotate, rot.get(), r.code, &q, a[2] != Py_None ? &k : nullptr, r.rows, wq, wk, off,
                     eps, r.pos, r.call.stream(a[10]));
@@ -248,6 +292,22 @@ PyObject* py_head_norm_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* K = r.call.flat(kc, "K_loc", cache, r.type);
     void* V = r.call.flat(a[9], "V_loc", cache, r.type);
     const float eps = (float)number(a[10]), off = (float)number(a[11]);
+    const Apart t{r.rows, D, r.q.element_size()};
+    const Place q_in = t.in(q), k_in = t.in(k), v_in = t.in(v), q_out = t.out(q), at = t.vec(slots, r.rows * 4);
+    t.small(q_out, "out", r.pos, wq, wk);
+    t.check(q_out, "out", at, "slots");
+    t.check(q_out, "out", k_in, "k");
+    t.check(q_out, "out", v_in, "v");
+    for (int i = 0; i < 2; ++i) {
+      const char* name = i ? "V_loc" : "K_loc";
+      const Place c = t.vec(i ? V : K, kc.nbytes());
+      t.small(c, name, r.pos, wq, wk);
+      t.check(c, name, at, "slots");
+      t.check(c, name, q_in, "q");
+      t.check(c, name, k_in, "k");
+      t.check(c, name, v_in, "v");
+      t.check(c, name, q_out, "out");
+    }
     r.call.on_current_device("q");
     return unlocked(entry.head_norm_append, rot.get(), r.code, &q, &k, &v, r.rows, wq, wk, off, eps, r.pos, slots, K, V,
                     (int32_t)cache[0], (int32_t)cache[1], r.call.stream(a[13]));
@@ -292,6 +352,23 @@ PyObject* py_head_norm_rotate_grad(PyObject*, PyObject* const* a, Py_ssize_t n) 
     size_t bytes;
     workspace(a[14], &ws, &bytes);
     if (tensor(a[14], "ws").device() != r.call.dev) refuse("ws: expected on %s", r.call.dev.str().c_str());
+    const Apart t{r.rows, D, r.q.element_size()};
+    const Place q_in = t.in(q), gq = t.out(dq), sums[2] = {t.vec(gwq, D * 4), t.vec(gwk, D * 4)};
+    t.small(gq, "out[0]", r.pos, wq, wk);
+    if (!msa::same_blocks(gq, q_in)) t.check(gq, "out[0]", q_in, "q");  // in place: a lane reads its elements of both first
+    if (has_k) {
+      const Place k_in = t.in(k), gk = t.out(dk);
+      t.small(gk, "out[1]", r.pos, wq, wk);
+      if (!msa::same_blocks(gk, k_in)) t.check(gk, "out[1]", k_in, "k");
+      t.check(gq, "out[0]", k_in, "k");
+      t.check(gq, "out[0]", t.in(dk), "dk");
+      t.check(gk, "out[1]", q_in, "q");
+      t.check(gk, "out[1]", t.in(dq), "dq");
+      t.check(gq, "out[0]", gk, "out[1]");
+      for (const Place& w : sums) t.check(w, "a weight's gradient", gk, "out[1]");
+    }
+    for (const Place& w : sums) t.check(w, "a weight's gradient", gq, "out[0]");
+    t.check(sums[0], "out[2]", sums[1], "out[3]");
     r.call.on_current_device("q");
     return unlocked(entry.head_norm_rotate_grad, rot.get(), r.code, &q, has_k ? &k : nullptr, &dq,
                     has_k ? &dk : nullptr, r.rows, wq, wk, off, eps, r.pos, gwq, gwk, ws, bytes, r.call.stream(a[15]));

@@ -10,10 +10,6 @@ struct Blocks {
   int64_t rows, heads, row, head, width;
 };
 
-inline Blocks range_of(const void* p, int64_t bytes) {
-  return {reinterpret_cast<uintptr_t>(p), p ? 1 : 0, 1, 0, 0, bytes};
-}
-
 // the same blocks at the same places
 inline bool same_blocks(const Blocks& a, const Blocks& b) {
   return a.base == b.base && a.rows == b.rows && a.heads == b.heads && a.width == b.width &&

@@ -231,3 +231,75 @@ def test_an_output_that_overlaps_its_input_is_refused(msa, monkeypatch, form, dt
     assert call(D, (8 * D, 2 * D), (8 * D, 2 * D)) == 4  # heads side by side
     assert call(0, (0, 0), flat) == 1                  # a broadcast input inside its output
     assert call(heads * D, (0, 0), flat) == 4
+
+
+def test_the_binding_refuses_outputs_inside_other_tensors(msa):
+    """Outputs that share memory with another output or input of the call.  (Host tensors: what fits is told
+    that it wants CUDA tensors.)"""
+    import torch
+
+    def fits(f, *a, **kw):
+        with pytest.raises(ValueError, match="CUDA"):
+            f(*a, **kw)
+
+    def clash(f, *a, **kw):
+        with pytest.raises(ValueError, match="overlap"):
+            f(*a, **kw)
+
+    R, D, r = 6, 64, msa.rotary(64)
+    fused = torch.zeros(R, 12, D)  # 8 query, 2 key, 2 value heads of one projection
+    q, k, v = fused[:, :8], fused[:, 8:10], fused[:, 10:]
+    pos, slots = torch.zeros(R, dtype=torch.int32), torch.zeros(R, dtype=torch.int32)
+    w = torch.ones(D)
+    new = torch.empty_like
+    for f, a in ((msa.rotate, (r, q, pos)), (lambda *x, k, **kw: msa.head_norm_rotate(x[0], x[1], k, w, w, x[2], **kw), (r, q, pos))):
+        fits(f, *a, k=k, out=q, k_out=k)                  # both in place
+        fits(f, *a, k=k, out=new(q), k_out=new(k))
+        fits(f, *a, k=fused[:, :2], out=new(q))           # inputs may share
+        clash(f, *a, k=k, k_out=q[:, 2:4])                # the keys' output inside the queries
+        clash(f, *a, k=k, out=fused[:, 4:])               # the queries' output over the keys
+        o = torch.zeros(R, 8, D)
+        clash(f, *a, k=k, out=o, k_out=o[:, 6:])
+        clash(f, *a, k=k, out=o, k_out=o.view(-1)[D:D + R * 2 * D].view(R, 2, D))
+        store = torch.zeros(R * 8 * D)                    # positions inside an output
+        clash(f, r, q, store.view(torch.int32)[D:D + R], k=k, out=store.view(R, 8, D))
+    clash(msa.head_norm_rotate, r, q, None, fused[2, 3], None, pos, out=q)  # a weight inside the output
+    K, V = torch.zeros(2, 9, 2, D), torch.zeros(2, 9, 2, D)
+    app = lambda q=q, k=k, v=v, K=K, V=V, w=w, pos=pos, slots=slots, **kw: msa.head_norm_append(r, q, k, v, w, w, pos, slots, K, V, **kw)
+    fits(app, out=q)
+    fits(app)
+    clash(app, out=fused[:, 2:10])
+    clash(app, out=fused[:, 4:])
+    for name in ("K", "V"):
+        cache = torch.zeros(2, 9, 2, D)
+        rows = cache.view(18, 2, D)[:R]
+        wide = cache.view(-1)[:R * 2 * D].view(R, 2, D)
+        clash(app, **{name: cache}, k=rows)
+        clash(app, **{name: cache}, v=rows)
+        clash(app, **{name: cache}, q=wide)
+        clash(app, **{name: cache}, q=wide, out=new(wide))
+        clash(app, **{name: cache}, q=k, out=wide)
+        clash(app, **{name: cache}, w=cache.view(-1)[64:128])
+        clash(app, **{name: cache}, pos=cache.view(torch.int32).view(-1)[:R])
+        clash(app, **{name: cache}, slots=cache.view(torch.int32).view(-1)[-R:])
+    g = torch.zeros(R, 12, D)
+    dq, dk = g[:, :8], g[:, 8:10]
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    W = lambda: torch.zeros(D)
+    back = lambda out, w=w: msa.head_norm_rotate_grad(r, q, k, w, w, pos, dq, dk, out=out, ws=ws)
+    fits(back, (new(q), new(k), W(), W()))
+    fits(back, (dq, dk, W(), W()))                        # over the outputs' gradients
+    fits(back, (q, k, None, None))                        # over the inputs
+    clash(back, (fused[:, 1:9], new(k), W(), W()))
+    clash(back, (new(q), dq[:, :2], W(), W()))
+    clash(back, (new(q), q[:, :2], W(), W()))
+    clash(back, (g[:, 4:], new(k), W(), W()))
+    clash(back, (fused[:, 4:], new(k), W(), W()))
+    o = torch.zeros(R, 8, D)
+    clash(back, (o, o[:, :2], W(), W()))
+    clash(back, (o, new(k), o[2, 3], W()))
+    clash(back, (new(q), o[:, :2], W(), o[5, 1]))
+    x = torch.zeros(2 * D)
+    clash(back, (new(q), new(k), x[:D], x[1:D + 1]))
+    clash(back, (o, new(k), None, None), w=o[1, 1])
+    fits(back, (new(q), new(k), x[:D], x[D:]))
