@@ -1,7 +1,9 @@
 """Build libmsa.so (the C-ABI library) in-tree with nvcc for sm_100a, and _fastcall (the binding's checks
-of latency-bound calls) with the host compiler against PyTorch's headers."""
+of latency-bound calls) with the host compiler against PyTorch's headers.  The library needs nvcc alone:
+without PyTorch it is built, and the binding's part is left out."""
 from __future__ import annotations
 
+import importlib.util
 import os
 import subprocess
 import sys
@@ -17,9 +19,10 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(FAST):
+    built = [LIB] + ([FAST] if importlib.util.find_spec("torch") else [])
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(FAST))
+    t = min(os.path.getmtime(f) for f in built)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(ROOT, "include", "msa.h")]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -42,7 +45,8 @@ def fastcall_command() -> list:
 
 
 def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile every source to an object in parallel (relocatable device code), then link libmsa.so."""
+    """Compile every source to an object in parallel (relocatable device code), then link libmsa.so;
+    beside them _fastcall.so, whose failure is raised once the library stands."""
     import concurrent.futures as cf
     import tempfile
 
@@ -53,7 +57,10 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
     with tempfile.TemporaryDirectory(prefix="msa_build_") as tmp:
         objs = [os.path.join(tmp, os.path.splitext(src)[0] + ".o") for src in SOURCES]
         cmds = [flags + ["-c", os.path.join(CSRC, src), "-o", obj] for src, obj in zip(SOURCES, objs)]
-        cmds.append(fastcall_command())
+        try:
+            cmds.append(fastcall_command())
+        except ImportError as e:
+            sys.stderr.write(f"_fastcall.so is left out ({e}): the binding's rotation, norm and draft-tree calls need it\n")
         if verbose:
             for c in cmds:
                 print(" ".join(c), flush=True)
@@ -62,9 +69,10 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         for r in results:
             if r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
-                raise RuntimeError("compiling libmsa.so or _fastcall.so failed")
-            if verbose or ptxas_verbose:
+            elif verbose or ptxas_verbose:
                 sys.stderr.write(r.stderr)
+        if any(r.returncode != 0 for r in results[:len(objs)]):
+            raise RuntimeError("nvcc failed building libmsa.so")
         link = [NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-rdc=true", "-shared", "-Xcompiler", "-fPIC",
                 "-cudart", "static", "-o", LIB] + objs
         if verbose:
@@ -73,6 +81,8 @@ def build(verbose: bool = False, ptxas_verbose: bool = False) -> str:
         if r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("nvcc failed linking libmsa.so")
+        if any(r.returncode != 0 for r in results[len(objs):]):
+            raise RuntimeError("libmsa.so is built, but compiling _fastcall.so failed")
     return LIB
 
 

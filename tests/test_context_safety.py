@@ -303,3 +303,53 @@ def test_the_binding_refuses_outputs_inside_other_tensors(msa):
     clash(back, (new(q), new(k), x[:D], x[1:D + 1]))
     clash(back, (o, new(k), None, None), w=o[1, 1])
     fits(back, (new(q), new(k), x[:D], x[D:]))
+
+
+@pytest.fixture
+def commands(monkeypatch):
+    """The build's commands, recorded instead of run; those that name a word of ``fail`` fail."""
+    from long_context_memory_b200 import build
+
+    class Done:
+        returncode, stdout, stderr = 0, "", ""
+
+    seen, fail = [], []
+
+    def run(cmd, **kw):
+        seen.append(cmd)
+        d = Done()
+        d.returncode = int(any(w in str(c) for c in cmd for w in fail))
+        return d
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return build, seen, fail
+
+
+def _linked(build, seen):
+    return [i for i, c in enumerate(seen) if build.LIB in c]
+
+
+def test_the_library_builds_without_pytorch(commands, monkeypatch, capsys):
+    """libmsa.so needs nvcc alone: the C ABI's users need no PyTorch."""
+    import sys
+
+    build, seen, fail = commands
+    for name in {"torch"} | {m for m in sys.modules if m.startswith("torch.")}:
+        monkeypatch.setitem(sys.modules, name, None)
+    assert build.build() == build.LIB
+    assert len(_linked(build, seen)) == 1 and not any(build.FAST in c for c in seen)
+    assert "_fastcall" in capsys.readouterr().err  # and it says what was left out
+    monkeypatch.setattr(build.importlib.util, "find_spec", lambda name: None)
+    monkeypatch.setattr(build, "FAST", build.FAST + ".missing")
+    assert not build.needs_build()  # a library alone is up to date then
+
+
+def test_the_library_is_linked_although_the_binding_s_part_fails(commands):
+    build, seen, fail = commands
+    fail.append("fastcall.cpp")
+    with pytest.raises(RuntimeError, match="_fastcall"):
+        build.build()
+    assert len(_linked(build, seen)) == 1
+    fail[:] = ["tree.cu"]
+    with pytest.raises(RuntimeError, match="libmsa"):
+        build.build()
