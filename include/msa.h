@@ -559,8 +559,8 @@ msa_status msa_rope_cache_build(const msa_dims* dims, int32_t t_loc_max, int32_t
  *              at(t) = R ln(orig_len / (2 pi t)) / (2 ln base),
  *              first = max(floor(at(high)), 0), last = min(ceil(at(low)), R - 1),
  *              g = 1 - clamp((i - first) / (last - first), 0, 1) (0.001 for an empty ramp)
- *   magnitude  multiplies cosine and sine (1 = a plain rotation; YaRN's attention
- *              temperature is 0.1 ln(factor) + 1).
+ *   magnitude  multiplies cosine and sine (1 = a plain rotation).  No scaling sets it by itself: a
+ *              checkpoint trained with YaRN's attention temperature wants 0.1 ln(factor) + 1 here.
  *   Rotation: (a, b) -> m (a cos - b sin, b cos + a sin), m = magnitude.
  * The frequencies are computed on the host in extended precision; the angle is
  * reduced exactly (a 64-bit fraction of a turn), whatever the position's size.
@@ -576,6 +576,16 @@ msa_status msa_rope_cache_build(const msa_dims* dims, int32_t t_loc_max, int32_t
  * element only; the kernels take 16-byte accesses where pointers, strides and
  * rot_dim allow them.
  * dtype: type of every head tensor and weight of the call.
+ *
+ * What goes with what.  msa_sparse_attend, its shares and msa_tiered_decode take queries and new keys BEFORE
+ * RoPE and turn them themselves: whole heads, half layout, base dims->rope_base, no scaling.  With a
+ * backbone of that position code and per-head norms, normalise its heads by msa_head_norm_rotate at
+ * positions 0, where nothing is turned (magnitude 1), and pass those (one more rounding to the type).
+ * Heads turned by any other code go to msa_tree_attend, with caches that msa_head_norm_append,
+ * msa_rotate or msa_tree_commit filled.  The pooled keys are msa_encode_memory's either way: turned by the plain
+ * code at positions inside their document, and not normalised.  Queries meet them as they are, so a
+ * backbone with another code or with norms has to have been trained against such a memory, or brings
+ * a memory of its own (K̄ in the same layout).
  * ------------------------------------------------------------------------- */
 typedef enum { MSA_BF16 = 0, MSA_FP16 = 1, MSA_FP32 = 2 } msa_dtype;
 enum { MSA_LAYOUT_HALF = 0, MSA_LAYOUT_INTERLEAVED = 1 };
@@ -626,6 +636,8 @@ msa_status msa_head_norm_rotate(const msa_rotary* rot, msa_dtype dtype, const ms
  * normalised and rotated, and its value heads v (copied) go to the local cache:
  * row r belongs to query r / (rows / B) and is written at slot slots[r]:
  *   K_loc[b, slots[r]] = y_k[r],  V_loc[b, slots[r]] = v[r].
+ * The queries come out ROTATED: they are for msa_tree_attend (a step of one token is a tree of one draft),
+ * not for msa_sparse_attend and msa_tiered_decode, which rotate their query and new key themselves (see above).
  * K_loc, V_loc [B, t_loc_max, k->heads, head_dim] of the call's dtype, contiguous;
  * k->out and v->out are unused.  slots [rows] device int32: -1 leaves the row out
  * of the cache (a padded row); another slot outside [0, t_loc_max) is left out too

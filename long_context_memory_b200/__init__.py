@@ -556,7 +556,8 @@ def rotary(head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", b
     (``layout`` "half") or (2i, 2i + 1) ("interleaved") by position * theta_i, theta_i =
     base^(-2i/rot_dim), ``scaling`` one of "none", "linear", "ntk", "parts" (mixed by turns over
     ``orig_len`` tokens between ``low`` and ``high``) and "yarn" (the same mix over the pair's
-    index), by ``factor``; cosine and sine are multiplied by ``magnitude`` (see msa.h)."""
+    index), by ``factor``; cosine and sine are multiplied by ``magnitude`` (see msa.h).  "yarn" leaves the
+    magnitude to the caller: its attention temperature is ``0.1 * math.log(factor) + 1``."""
     if layout not in _LAYOUTS:
         raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, got {layout!r}")
     if scaling not in _SCALINGS:
@@ -666,7 +667,8 @@ def head_norm_append(rot: Rotary, q, k, v, q_weight, k_weight, positions, slots,
     """``head_norm_rotate`` of a decode or prefill step: the queries go to ``out``, the keys
     (normalised, rotated) and the values to row ``slots[r]`` of their query's local cache
     K_loc, V_loc [B, t_loc_max, n_kv, head_dim] (rows / B rows per query, in order).  A slot of -1
-    leaves the row out of the cache.  Returns out."""
+    leaves the row out of the cache.  Returns out: rotated queries, for ``tree_attend`` (``sparse_attend``
+    and ``tiered_decode`` turn theirs themselves: give them heads normalised at positions 0)."""
     fast = _fast or _load_fast()
     if out is None:
         out = _like(q) if stream is None else _made(stream, lambda: _like(q))

@@ -123,3 +123,46 @@ def test_other_threads_run_beside_a_call(msa, cuda_device, tmp_path):
     subprocess.run(["g++", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
     r = subprocess.run([sys.executable, "-c", BESIDE, ROOT, str(so)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("D,n_q,n_kv", [(64, 8, 2), (128, 32, 8)])
+def test_normalised_heads_in_the_decode_attention(msa, cuda_device, D, n_q, n_kv):
+    """sparse_attend rotates its query and its new key itself: it takes heads that head_norm_rotate normalised
+    at position 0, where nothing is turned.  The norm is rounded once (2^-8 of its value, and fp32 arithmetic
+    within 2^-19 of it); the attention has its own tolerance on the heads that it was given."""
+    import torch
+
+    import context_oracle as C
+    import oracle as O
+    from long_context_memory_b200 import workloads as W
+
+    rng = np.random.default_rng(D)
+    B, T, off = 2, 40, 5
+    dev, dims = cuda_device, W.Dims(hidden=256, n_q=n_q, n_kv=n_kv, head_dim=D, n_r=4, d_r=64)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(dev).to(torch.bfloat16)
+    bits = lambda t: t.cpu().view(torch.int16).numpy().view(np.uint16)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)
+    fused, wq, wk = bf(B, n_q + 2 * n_kv, D), bf(D), bf(D)
+    q0, k0, v = fused[:, :n_q], fused[:, n_q:n_q + n_kv], fused[:, n_q + n_kv:].contiguous()
+    rot = msa.rotary(D, base=dims.rope_base)
+    q, k = msa.head_norm_rotate(rot, q0, k0, wq, wk, i32([0] * B))
+    f64 = lambda t: t.cpu().double().numpy()
+    for x, w, y in ((q0, wq, q), (k0, wk, k)):
+        n = C.head_norm(f64(x), f64(w))
+        assert np.all(np.abs(f64(y) - n) <= (2.0 ** -8 + 2.0 ** -19) * np.abs(n) + 1e-30)
+    co, idx, loc = np.array([0, 4, 9, 11], dtype=np.int32), np.array([[2, 0], [1, 2]], dtype=np.int32), np.array([T, 7], dtype=np.int32)
+    Kb, Vb, K, V = bf(11, n_kv, D), bf(11, n_kv, D), bf(B, T, n_kv, D), bf(B, T, n_kv, D)
+    Kr = msa.rotate(rot, K.view(B * T, n_kv, D), (torch.arange(T, device=dev, dtype=torch.int32) + off).repeat(B)).view(K.shape)
+    Vr = V.clone()
+    got = msa.sparse_attend(dims, q, Kb, Vb, i32(co), i32(idx), Kr, Vr, i32(loc), off, k_loc_rotated=True, k_new=k, v_new=v)
+    for b in range(B):
+        K[b, loc[b] - 1], V[b, loc[b] - 1] = k[b], v[b]
+    ref = O.sparse_attend(bits(q), bits(Kb), bits(Vb), co, idx, bits(K), bits(V), loc, off, dims.rope_base)
+    err = np.abs(f64(got.view(B, n_q, D)) - ref)
+    assert np.all(err <= 2e-2 + 2e-2 * np.abs(ref)) and msa.check_device_errors() == 0
+    # the token's key stands in the cache as head_norm_rotate turns it, but for one more rounding
+    _, at = msa.head_norm_rotate(rot, q0, k0, wq, wk, i32(loc - 1 + off))
+    for b in range(B):
+        a = np.abs(f64(k[b]))
+        pair = a + np.roll(a, D // 2, axis=-1)
+        assert np.all(np.abs(f64(Kr[b, loc[b] - 1]) - f64(at[b])) <= (3 * 2.0 ** -8 + 2.0 ** -18) * pair)
