@@ -770,11 +770,13 @@ msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall&
     p.its += h.its;
     p.classes = i + 1;
   }
-  // Shares of a row: every SM's warps when there are few rows, and, for the forward kernels, several
-  // rounds of the persistent warps (a round that is half empty costs the share of a round that it
-  // leaves idle: 8193 rows of 40 heads in fp32, 3.5 rounds, 68 us whole and 63 us in two shares; the
-  // gradients lose more on the second angle table of a row than that, 61 against 67 us)
-  const int64_t want = (c.mode == 2 ? 16LL : 96LL) * sm_count();
+  // Shares of a row: enough warps for every SM when there are few rows (2368 here), whole rows beyond, since each
+  // share makes the row's angles and factors again.  More shares, to fill the persistent warps' last round (up
+  // to 14208), cost most sizes more than that round: 40 heads of 128, norm and rotation of 1500, 6000 and
+  // 14000 bf16 rows 21.5, 39.7 and 77.8 us against 14.7, 30.6 and 59.0 so, rotation alone 19.0, 33.9 and 65.4
+  // against 12.6, 26.5 and 52.8, in fp32 18.4, 47.9 and 102.3 against 16.9, 47.9 and 100.1 (and gain 2 to 8% in
+  // fp32 between 3000 and 10000 rows alone).
+  const int64_t want = 16LL * sm_count();
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.its, (want + p.rows - 1) / std::max<int64_t>(1, p.rows)));
   int ctas = 0;
   if (c.mode == 2) {
