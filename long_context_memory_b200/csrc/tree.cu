@@ -164,7 +164,11 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;        // keys per tile, rows per row tile
 constexpr int kMaxRing = 6;
-constexpr int kSmallB = 32;       // queries whose tile counts every CTA computes itself
+// Queries whose documents' rows every CTA counts itself; beyond, a kernel of their own counts them once.
+// 8 drafts over 256 local tokens, 32/8 heads of 128, counted by every CTA against by the kernel: 4 queries of
+// 16 documents 18.1 against 19.0 us, 8 of 2 21.4 against 22.5, 8 of 16 23.8 against 23.9, 8 of 64 33.5
+// against 31.0, 16 of 1 27.6 against 26.4, 16 of 16 32.4 against 28.7, 32 of 16 49.7 against 40.1.
+constexpr int kSmallB = 8;
 constexpr float kSlack = 8.f;
 constexpr int kTmemCols = 512;    // scores 2 x 128, outputs 2 x 128
 

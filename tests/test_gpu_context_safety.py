@@ -6,7 +6,7 @@ import sys
 import numpy as np
 import pytest
 
-from test_gpu_tree import _case, _run
+from test_gpu_tree import _case, _check, _run
 
 pytestmark = pytest.mark.gpu
 
@@ -20,7 +20,7 @@ def msa(cuda_device):
     return m
 
 
-@pytest.mark.parametrize("B", [1, 32, 33, 70])
+@pytest.mark.parametrize("B", [1, 8, 9, 32, 33, 70])
 @pytest.mark.parametrize("bad", ["only", "beside an empty one", "nothing drafted"])
 def test_bad_documents_are_reported_in_every_batch(msa, cuda_device, B, bad):
     """A document id out of range raises the device error whatever the batch, also where its query has
@@ -45,7 +45,7 @@ def test_bad_documents_are_reported_in_every_batch(msa, cuda_device, B, bad):
             msa.check_device_errors()
 
 
-@pytest.mark.parametrize("B,k", [(1, 2), (32, 1), (33, 1), (40, 0)])
+@pytest.mark.parametrize("B,k", [(1, 2), (8, 1), (9, 1), (33, 1), (40, 0)])
 def test_kernels_are_traced_under_their_own_names(msa, cuda_device, B, k):
     """The attention alone: no time of the plan's, and the counting of large batches' rows by its name."""
     c = _case(B, B, 3, 4, 2, 64, 20, np.full(B, 20), k, False, cuda_device)
@@ -58,7 +58,7 @@ def test_kernels_are_traced_under_their_own_names(msa, cuda_device, B, k):
     finally:
         msa.trace_enable(False)
     want = {"tree_attend": 1, "tree_combine": 1}
-    if B > 32 and k:
+    if B > 8 and k:
         want["tree_select"] = 1
     assert launches == want
 
@@ -166,3 +166,16 @@ def test_normalised_heads_in_the_decode_attention(msa, cuda_device, D, n_q, n_kv
         a = np.abs(f64(k[b]))
         pair = a + np.roll(a, D // 2, axis=-1)
         assert np.all(np.abs(f64(Kr[b, loc[b] - 1]) - f64(at[b])) <= (3 * 2.0 ** -8 + 2.0 ** -18) * pair)
+
+
+@pytest.mark.parametrize("B,M,n_q,n_kv,D,T,k", [(8, 5, 8, 2, 64, 200, 7), (9, 5, 8, 2, 64, 200, 7), (20, 40, 8, 2, 64, 150, 3),
+                                               (32, 3, 16, 8, 128, 90, 16), (12, 17, 32, 8, 128, 300, 0)])
+def test_batches_about_the_planning_s_limit(msa, cuda_device, B, M, n_q, n_kv, D, T, k):
+    """Ragged batches on both sides of the size from which a kernel counts the documents' rows."""
+    import torch
+
+    loc = np.random.default_rng(B).integers(0, T + 1, size=B)
+    c = _case(B + k, B, M, n_q, n_kv, D, T, loc, k, True, cuda_device)
+    got = _run(msa, c, cuda_device)
+    _check(got, c)
+    assert torch.equal(got, _run(msa, c, cuda_device)) and msa.check_device_errors() == 0
