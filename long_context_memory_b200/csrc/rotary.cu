@@ -770,13 +770,17 @@ msa_status rotary_launch(const msa_rotary& r, msa_dtype dtype, const RotaryCall&
     p.its += h.its;
     p.classes = i + 1;
   }
-  // Shares of a row: enough warps for every SM when there are few rows (2368 here), whole rows beyond, since each
-  // share makes the row's angles and factors again.  More shares, to fill the persistent warps' last round (up
-  // to 14208), cost most sizes more than that round: 40 heads of 128, norm and rotation of 1500, 6000 and
-  // 14000 bf16 rows 21.5, 39.7 and 77.8 us against 14.7, 30.6 and 59.0 so, rotation alone 19.0, 33.9 and 65.4
-  // against 12.6, 26.5 and 52.8, in fp32 18.4, 47.9 and 102.3 against 16.9, 47.9 and 100.1 (and gain 2 to 8% in
-  // fp32 between 3000 and 10000 rows alone).
-  const int64_t want = 16LL * sm_count();
+  // Shares of a row.  Fewer rows than persistent warps (2368 here): as many as give every warp work.  Beyond, whole
+  // rows, since each share makes the row's angles and factors again: more of them, up to 14208 warps,
+  // cost 40 bf16 heads of 128 (10 iterations) 39.7 against 30.6 us at 6000 rows normalised and rotated and 33.9
+  // against 26.5 rotated alone.  But long rows (20 iterations were measured) go in two shares where that saves
+  // half of the last of up to four rounds: 3000, 5001 and 8193 rows of 40 fp32 heads of 128 rotated in 26.4, 41.7
+  // and 61.3 us against 29.5, 43.7 and 63.8, normalised too 29.7, 46.5 and 66.5 against 34.1, 48.8 and 68.6,
+  // of 80 bf16 heads rotated 27.8, 43.2 and 63.2 against 31.4, 44.4 and 65.5; where it saves none they lose (4000 and
+  // 6000 rows in fp32 34.2 and 48.7 against 32.6 and 48.0), and the gradients lose throughout.
+  const int64_t warps = 16LL * sm_count(), rounds = (p.rows + warps - 1) / warps;
+  const bool halves = c.mode != 2 && p.its >= 20 && rounds >= 2 && rounds <= 4 && (2 * p.rows + warps - 1) / warps < 2 * rounds;
+  const int64_t want = halves ? 2 * p.rows : warps;
   p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(p.its, (want + p.rows - 1) / std::max<int64_t>(1, p.rows)));
   int ctas = 0;
   if (c.mode == 2) {

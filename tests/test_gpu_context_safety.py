@@ -179,3 +179,22 @@ def test_batches_about_the_planning_s_limit(msa, cuda_device, B, M, n_q, n_kv, D
     got = _run(msa, c, cuda_device)
     _check(got, c)
     assert torch.equal(got, _run(msa, c, cuda_device)) and msa.check_device_errors() == 0
+
+
+@pytest.mark.parametrize("rows", [2367, 2369, 4000, 8193])
+@pytest.mark.parametrize("form", ["rotate", "norm"])
+def test_long_rows_in_shares(msa, cuda_device, rows, form):
+    """Rows that are taken whole or in two shares: a row's result does not depend on the rows beside it."""
+    import torch
+
+    gen = torch.Generator(device=cuda_device).manual_seed(rows)
+    rn = lambda *s: torch.randn(*s, generator=gen, device=cuda_device)
+    q, k, w = rn(rows, 32, 128), rn(rows, 7, 128), rn(128)
+    p = torch.randint(0, 1 << 20, (rows,), generator=gen, device=cuda_device, dtype=torch.int32)
+    rot = msa.rotary(128, 64, layout="interleaved")
+    f = (lambda q, k, p: msa.rotate(rot, q, p, k=k)) if form == "rotate" else (lambda q, k, p: msa.head_norm_rotate(rot, q, k, w, w, p))
+    out = f(q, k, p)
+    for lo in range(0, rows, 100):
+        part = f(q[lo:lo + 100], k[lo:lo + 100], p[lo:lo + 100])
+        assert torch.equal(out[0][lo:lo + 100], part[0]) and torch.equal(out[1][lo:lo + 100], part[1])
+    assert msa.check_device_errors() == 0
