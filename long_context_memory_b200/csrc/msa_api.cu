@@ -1188,7 +1188,10 @@ msa_status msa_tree_attend(const msa_dims* dims, const void* q, const void* K_dr
   const size_t row = (size_t)dims->n_kv * dims->head_dim * 2, rows = (size_t)B * M * dims->n_q * dims->head_dim * 2;
   if (overlap(out, rows, q, rows) || overlap(out, rows, K_draft, B * M * row) || overlap(out, rows, V_draft, B * M * row) ||
       (t_loc_max > 0 && (overlap(out, rows, K_loc, (size_t)B * t_loc_max * row) || overlap(out, rows, V_loc, (size_t)B * t_loc_max * row))) ||
-      (k > 0 && (overlap(out, rows, K_bar, n_chunks * row) || overlap(out, rows, V_bar, n_chunks * row))))
+      (k > 0 && (overlap(out, rows, K_bar, n_chunks * row) || overlap(out, rows, V_bar, n_chunks * row) ||
+                 overlap(out, rows, chunk_off, ((size_t)n_docs + 1) * 4) || overlap(out, rows, topk_idx, (size_t)B * k * 4))) ||
+      overlap(out, rows, mask, (size_t)B * M * ((M + 31) / 32) * 4) || overlap(out, rows, loc_len, (size_t)B * 4) ||
+      overlap(out, rows, n_draft, (size_t)B * 4))
     return fail(MSA_ERR_INVALID_ARG, "out must not overlap the inputs");
   const size_t need = tree_attend_workspace(*dims, B, M, k, t_loc_max);
   if (ws_bytes < need) return fail(MSA_ERR_WORKSPACE, "workspace too small: %zu < %zu bytes", ws_bytes, need);

@@ -353,3 +353,26 @@ def test_the_library_is_linked_although_the_binding_s_part_fails(commands):
     fail[:] = ["tree.cu"]
     with pytest.raises(RuntimeError, match="libmsa"):
         build.build()
+
+
+def test_the_tree_attention_s_output_stays_off_its_small_inputs(msa, monkeypatch):
+    """out over the mask, the lengths, the documents or the routing: other CTAs would read what was written."""
+    import ctypes
+
+    monkeypatch.setenv("MSA_FAULT", "launch")
+    d = msa.Dims(64, 8, 2, 64, 1, 64, 64, 1e6)
+    B, M, T, k, n_docs, n_chunks = 2, 40, 10, 3, 50, 90
+    need = msa.lib.msa_tree_attend_workspace_size(ctypes.byref(d), B, M, k, T)
+    far = FAKE + (1 << 40)
+
+    def call(out=far, mask=FAKE, n_draft=None, loc=FAKE, off=FAKE, top=FAKE):
+        return msa.lib.msa_tree_attend(ctypes.byref(d), FAKE, FAKE, FAKE, mask, n_draft, B, M, FAKE, FAKE, loc, T, FAKE, FAKE, off,
+                                       n_docs, n_chunks, top, k, 0.0, out, FAKE, need, None)
+
+    size = B * M * 8 * 64 * 2
+    assert call() == 4
+    for name, n in (("mask", B * M * 2 * 4), ("n_draft", B * 4), ("loc", B * 4), ("off", (n_docs + 1) * 4), ("top", B * k * 4)):
+        assert call(**{name: far + size}) == 4, name          # right behind
+        assert call(**{name: far + size - 16}) == 1, name
+        assert call(**{name: far - (n + 15) // 16 * 16}) == 4, name
+        assert call(**{name: far - n // 16 * 16 + (0 if n % 16 else 16)}) == 1, name
