@@ -198,3 +198,37 @@ def test_long_rows_in_shares(msa, cuda_device, rows, form):
         part = f(q[lo:lo + 100], k[lo:lo + 100], p[lo:lo + 100])
         assert torch.equal(out[0][lo:lo + 100], part[0]) and torch.equal(out[1][lo:lo + 100], part[1])
     assert msa.check_device_errors() == 0
+
+
+def test_two_threads_call_at_once(msa, cuda_device):
+    """Calls of two Python threads, each on a stream of its own, give what one thread's calls give."""
+    import threading
+
+    import torch
+
+    cs = [_case(41, 2, 24, 16, 4, 64, 900, [900, 333], 3, False, cuda_device), _case(42, 12, 9, 8, 2, 128, 200, [1, 199] * 6, 2, True, cuda_device)]
+    rots = [msa.rotary(64, scaling="linear", factor=2.0), msa.rotary(64, 32, layout="interleaved")]
+    x = torch.randn(50, 8, 64, device=cuda_device, dtype=torch.bfloat16)
+    pos = torch.arange(50, device=cuda_device, dtype=torch.int32)
+    ref = [(_run(msa, c, cuda_device), msa.rotate(r, x, pos)) for c, r in zip(cs, rots)]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            with torch.cuda.stream(st):
+                for _ in range(60):
+                    got[i].append((_run(msa, cs[i], cuda_device), msa.rotate(rots[i], x, pos)))
+            st.synchronize()
+        except Exception as e:  # (a thread's exception is the test's)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    assert all(torch.equal(a, ref[i][0]) and torch.equal(b, ref[i][1]) for i in range(2) for a, b in got[i])
+    assert len(got[0]) == len(got[1]) == 60 and msa.check_device_errors() == 0
