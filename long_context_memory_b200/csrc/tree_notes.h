@@ -25,8 +25,10 @@ struct MergeNote {
 // that passes reads parts and writes output rows inside their buffers and ends: query, draft and head
 // index the output, groups and slot the parts.
 MSA_HOST_DEVICE bool merge_note_ok(const MergeNote& n, int B, int M, int n_kv, int groups) {
-  return n.query >= 0 && n.query < B && n.draft >= 0 && n.draft < M && n.head >= 0 && n.head < n_kv && n.first >= 0 &&
-         n.first < n.last && n.last < groups && n.slot >> 1 == n.first * n_kv + n.head;
+  // (unsigned: a negative number is out of range too; one predicate, no chain of branches)
+  const auto below = [](int v, int end) { return static_cast<unsigned>(v) < static_cast<unsigned>(end); };
+  return below(n.query, B) & below(n.draft, M) & below(n.head, n_kv) & below(n.first, n.last) & below(n.last, groups) &
+         (n.slot >> 1 == n.first * n_kv + n.head);
 }
 
 }  // namespace msa
