@@ -9,8 +9,8 @@
 // All of them read each head once and write it once, a few dozen operations per element: bound by
 // HBM at the large sizes and by the launch at the small ones.  Measured: the transposed rotation of
 // 8193 rows of 40 fp32 heads of 128 (336 MB) 64.6 us, 5.2 TB/s; norm and rotation of 16384 rows of 40
-// bf16 heads of 128 (336 MB) 70 us, 4.8 TB/s (a plain copy of the same bytes: 55 us; here the issue
-// slots are 53% busy as well); the gradients of 8191 rows of 40 fp16 heads of 96 (189 MB) 62 us, 3.1
+// bf16 heads of 128 (336 MB) 70 us, 4.8 TB/s (a plain copy of the same bytes: 53 us, 6.3 TB/s; here the
+// issue slots are 53% busy as well); the gradients of 8191 rows of 40 fp16 heads of 96 (189 MB) 62 us, 3.1
 // TB/s, bound by the arithmetic of a head group and its dependences; one row 2.8 us, a decode step of 16
 // rows with its cache 3.4 us on the device, of which the launch is most.
 //
@@ -631,7 +631,8 @@ int grad_ctas(int64_t rows, int its) {
 template <typename T, int V, int J>
 cudaError_t launch_forward(const RotP& p, bool norm, cudaStream_t s) {
   const int64_t warps = p.rows * p.parts;
-  // few warps: a small CTA on each of many SMs; many: 8 warps per CTA, persistent, kRotCtas CTAs per SM
+  // few warps: a small CTA on each of many SMs (40 bf16 heads of 128, 1 to 16 rows: 3.0-3.2 us, in CTAs of 8 warps
+  // 3.4-3.5); many: 8 warps per CTA, persistent, kRotCtas CTAs per SM
   const int wpc = warps >= 8LL * sm_count() ? 8 : (int)std::max<int64_t>(1, warps / sm_count());
   const dim3 grid((unsigned)std::min<int64_t>((warps + wpc - 1) / wpc, kRotCtas * sm_count()));
   auto kern = norm ? (p.interleaved ? rotate_kernel<T, V, J, true, true> : rotate_kernel<T, V, J, true, false>)

@@ -156,11 +156,14 @@ __global__ void __launch_bounds__(128) tree_commit_kernel(const uint4* __restric
 // tables, TMA), one MMA issuer.  One CTA per SM (its ring fills the shared memory).
 //
 // Measured (heads of 128, 32 query and 8 KV heads): 16 drafts of one query over 16 documents and 4K
-// local tokens 19.8 us, bound by the chain of a CTA's two to three tiles and the merge; 32 queries of 32
-// drafts over 8K tokens (1.17 GB) 246-261 us, 4.5-4.8 TB/s, on inputs that were not used just before, 212-220 us (5.4)
-// on such that were; 64 drafts of 32 queries 292 us, 940 TFLOP/s.  Heads of 64, 7 queries of up to 127 drafts over up
-// to 20K tokens: 59-72 us, bound by the softmax threads (about 3,050 cycles per key tile and two row
-// tiles, of which the weights take 1,700; a polynomial for a fifth to a third of the exponentials made it slower).
+// local tokens 20 us, bound by the chain of a CTA's two to three tiles and the merge; 32 queries of 32
+// drafts over 16 documents and 8K tokens (1.17 GB) 246-265 us, 4.4-4.8 TB/s, on inputs that were not used just
+// before, 204-220 us (5.3-5.7) on such that were; 32 queries of 64 drafts over 8K local tokens 295-298 us, 930 TFLOP/s.
+// Heads of 64, 7 queries of up to 127 drafts over up to 20K tokens: 59-81 us on different boxes, bound by the
+// softmax threads: a key tile against two row tiles takes 3,100 cycles, in which the exponentials of its
+// 256 x 128 scores are 2,048 (16 a cycle and SM, measured).  Of a stream's step its weights take 1,790 cycles beside
+// the other stream's, the maximum 400, the wait for the next scores 690.  (A polynomial on the FMA pipes for a
+// fifth to a third of the exponentials made it slower.)
 // ---------------------------------------------------------------------------
 constexpr int kTile = 128;        // keys per tile, rows per row tile
 constexpr int kMaxRing = 6;
@@ -684,8 +687,9 @@ __global__ void __launch_bounds__(320, 1) tree_attend_kernel(const __grid_consta
         }
         const bool k_there = k_ahead;
         // Heads of 128 have a ring of two or three tiles: the next tile's keys, where they are local rows,
-        // go before this one's values, whose place is free later (32 queries of 32 drafts over 8K tokens:
-        // 250 us against 262; heads of 64, with six tiles, lose 5% to the longer loop).
+        // go before this one's values, whose place is free later (32 queries of 32 drafts over 8K tokens
+        // 253 us against 262 on inputs that were not used just before, 204 against 207 on two taken in
+        // turns; heads of 64, with six tiles, gain nothing that stands out of their spread).
         k_ahead = D == 128 && t + 1 < hi && t + 1 >= Tc && t + 1 < Tc + Tl;
 #pragma unroll 1
         for (int kv = k_there ? 1 : 0; kv < 2; ++kv) {
@@ -1154,8 +1158,10 @@ cudaError_t launch_attend(const TreeMaps& maps, TreeP& p, cudaStream_t s) {
   TraceScope ts(kKTreeCombine, s);
   constexpr int kRows = 1024 / D;
   const int row_groups = NT == 1 ? (p.M * p.G + kRows - 1) / kRows : NT * 128 / kRows;
-  // many items: about two parts each, and many threads; few items: many parts, their loads in flight
-  // together
+  // Many items: about two parts each, and many threads; few items: many parts, their loads in flight
+  // together.  16 drafts, 32/8 heads of 128, two against sixteen ahead: 1 query over 4K local tokens 22.3 against
+  // 18.6 us, over 32K 45.3 against 43.4, 2 over 8K 32.1 against 31.4, 4 over 4K 33.0 against 34.4, 5 36.6 against 39.8,
+  // 8 48.8 against 53.8, 32 over 2K 73.3 against 80.8.
   const int n_items = p.B * p.n_rb * p.n_kv;
   auto merge = n_items * 4 > n_ctas ? tree_combine_kernel<D, NT, 2> : tree_combine_kernel<D, NT, 16>;
   return launch_pdl(merge, dim3(row_groups, p.by_item ? n_items : n_ctas), dim3(256), 0, s, p);
@@ -1193,6 +1199,8 @@ msa_status tree_commit_launch(const msa_dims& d, const void* K_draft, const void
                               const int32_t* loc_len, int t_loc_max, int32_t* new_len, cudaStream_t s) {
   TraceScope ts(kKTreeCommit, s);
   const int64_t items = (int64_t)B * A;
+  // warps per CTA, one against four: 1024 x 8 rows of 8 heads of 128 8.8 against 6.2 us, 256 x 17 4.8 against
+  // 4.4, 64 x 17 2.5 against 2.0; 16 x 9 and 1 x 5 the same 1.5
   const int wpc = items >= 4LL * sm_count() ? 4 : 1;
   MSA_CUDA_CHECK(launch_pdl(tree_commit_kernel, dim3((unsigned)((items + wpc - 1) / wpc)), dim3(32 * wpc), 0, s,
                             static_cast<const uint4*>(K_draft), static_cast<const uint4*>(V_draft), path, n_path, B, M,
