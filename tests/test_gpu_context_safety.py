@@ -111,7 +111,7 @@ for name, args in calls.items():
         steps += 1
     t.join()
     print(name, state, steps)
-    assert state == [0] and steps >= 10, name
+    assert state == [0] and steps >= 5, name
 """
 
 
